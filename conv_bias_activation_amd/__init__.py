@@ -9,6 +9,7 @@ this package raises ImportError — there is no fallback path.
     gemm_bias_act(A, B, bias, C, act="leaky_relu", alpha=0.001)
     conv2d_bias_act(x, w, bias, y, strides=(1, 1), pads=(0, 0, 0, 0), dilations=(1, 1), act="tanh")
     gemm_bias_act_2k(..., workspace=ws) / conv2d_bias_act_2k(..., workspace=ws)
+    mxfp4_quantize(X, codes, scales); gemm_mxfp4_bias_act(A, a_scales, B, b_scales, bias, C, act="gelu")
 """
 from ._binding import (  # noqa: F401
     ACT_CODES,
@@ -39,10 +40,15 @@ from ._binding import (  # noqa: F401
     gemm_bias_act_2k,
     gemm_bias_act_2k_noalloc,
     gemm_bias_act_workspace_size,
+    gemm_mxfp4_bias_act,
+    gemm_mxfp4_bias_add_act,
     gemm_tile_config,
     conv_tile_config,
     lib,
     lib_path,
+    mxfp4_dequantize,
+    mxfp4_quantize,
+    mxfp4_shapes,
     num_tile_configs,
     status_string,
     tile_config_name,

@@ -10,7 +10,7 @@ from typing import Optional, Sequence
 _HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_HERE, "libbiasact.so")
 
-DTYPE_CODES = {"f32": 0, "f16": 1, "bf16": 2, "i8": 3, "i32": 4}
+DTYPE_CODES = {"f32": 0, "f16": 1, "bf16": 2, "i8": 3, "i32": 4, "mxfp4": 5}
 ACT_CODES = {"none": 0, "relu": 1, "leaky_relu": 2, "tanh": 3, "gelu": 4, "sigmoid": 5}
 BA_OK, BA_ERR_INVALID, BA_ERR_UNSUPPORTED, BA_ERR_HIP = 0, 1, 2, 3
 
@@ -107,6 +107,17 @@ def _load():
     l.biasact_force_tile_config.restype = ctypes.c_int
     l.biasact_force_halo_variant.argtypes = [ctypes.c_int]
     l.biasact_force_halo_variant.restype = ctypes.c_int
+    u64p = ctypes.POINTER(ctypes.c_size_t)
+    l.mxfp4_packed_size.argtypes = [i64, i64, u64p, u64p]
+    l.mxfp4_packed_size.restype = ctypes.c_int
+    l.mxfp4_quantize.argtypes = [vp, vp, vp, i64, i64, ctypes.c_int, u32, vp]
+    l.mxfp4_quantize.restype = ctypes.c_int
+    l.mxfp4_dequantize.argtypes = l.mxfp4_quantize.argtypes
+    l.mxfp4_dequantize.restype = ctypes.c_int
+    l.gemm_mxfp4_bias_act.argtypes = [vp] * 6 + [i64, i64, i64, u32, ctypes.c_int, ctypes.c_float, vp]
+    l.gemm_mxfp4_bias_act.restype = ctypes.c_int
+    l.gemm_mxfp4_bias_add_act.argtypes = [vp] * 7 + [i64, i64, i64, u32, ctypes.c_int, ctypes.c_float, vp]
+    l.gemm_mxfp4_bias_add_act.restype = ctypes.c_int
     return l
 
 
@@ -458,6 +469,100 @@ def conv2d_bias_act_auto(x, w, bias, y, strides=(1, 1), pads=(0, 0, 0, 0), dilat
                                   _stream(stream))
     _check(rc, "conv2d_bias_act_auto")
     return y
+
+
+# -- MXFP4 ---------------------------------------------------------------------
+
+def mxfp4_shapes(rows: int, K: int):
+    """Shapes of the uint8 codes and scales of `rows` rows of K values."""
+    g = -(-int(K) // 128)
+    return (int(rows), 64 * g), (int(rows), 4 * g)
+
+
+def _packed(codes, scales, name):
+    """Groups of 128 values per row of an MXFP4 operand, checked."""
+    u8 = _torch().uint8
+    if codes.dtype != u8 or scales.dtype != u8:
+        raise ValueError(f"{name}: codes and scales must be uint8")
+    if codes.dim() != 2 or scales.dim() != 2:
+        raise ValueError(f"{name}: codes and scales must be 2-D")
+    g = scales.shape[1] // 4
+    if scales.shape[1] != 4 * g or tuple(codes.shape) != (scales.shape[0], 64 * g):
+        raise ValueError(f"{name}: codes must be [rows, 64 g] and scales [rows, 4 g], got "
+                         f"{tuple(codes.shape)} and {tuple(scales.shape)}")
+    return g
+
+
+def _mx_quant_args(X, codes, scales, axis, name):
+    if X.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if axis not in (0, 1):
+        raise ValueError("axis must be 0 or 1")
+    rows, K = X.shape if axis == 1 else (X.shape[1], X.shape[0])
+    _packed(codes, scales, "mxfp4")
+    if (tuple(codes.shape), tuple(scales.shape)) != mxfp4_shapes(rows, K):
+        raise ValueError(f"codes and scales must be {mxfp4_shapes(rows, K)}, got "
+                         f"{tuple(codes.shape)} and {tuple(scales.shape)}")
+    return rows, K, DTYPE_CODES[_tname(X)]
+
+
+def mxfp4_quantize(X, codes, scales, axis: int = 1, stream=None):
+    """Quantises X to MXFP4 with blocks of 32 along `axis`: the rows of
+    X[rows, K] (axis 1) or the columns of X[K, rows] (axis 0).  codes and
+    scales (uint8, mxfp4_shapes(rows, K)) are written and returned."""
+    rows, K, dt = _mx_quant_args(X, codes, scales, axis, "X")
+    rc = lib.mxfp4_quantize(_dev(X, "X"), _dev(codes, "codes"), _dev(scales, "scales"), rows, K, axis,
+                            dt, _stream(stream))
+    _check(rc, "mxfp4_quantize")
+    return codes, scales
+
+
+def mxfp4_dequantize(codes, scales, Y, axis: int = 1, stream=None):
+    """The values that codes and scales stand for, in Y's type and in Y's
+    layout ([rows, K] with axis 1, [K, rows] with axis 0)."""
+    rows, K, dt = _mx_quant_args(Y, codes, scales, axis, "Y")
+    rc = lib.mxfp4_dequantize(_dev(codes, "codes"), _dev(scales, "scales"), _dev(Y, "Y"), rows, K, axis,
+                              dt, _stream(stream))
+    _check(rc, "mxfp4_dequantize")
+    return Y
+
+
+def _gemm_mx_args(A, a_scales, B, b_scales, bias, C):
+    g = _packed(B, b_scales, "B")
+    if A.dim() != 2 or C.dim() != 2:
+        raise ValueError("A and C must be 2-D")
+    M, N = A.shape[0], B.shape[0]
+    if a_scales is not None:
+        K, ta = 128 * _packed(A, a_scales, "A"), "mxfp4"
+    else:
+        K, ta = A.shape[1], _tname(A)
+    if -(-K // 128) != g or tuple(C.shape) != (M, N):
+        raise ValueError(f"shape mismatch: A{tuple(A.shape)} B{tuple(B.shape)} C{tuple(C.shape)}")
+    if bias is not None and bias.numel() != N:
+        raise ValueError(f"bias must have N = {N} elements")
+    return M, N, K, dtypes_code(ta, "mxfp4", _tname(bias) if bias is not None else None, _tname(C))
+
+
+def gemm_mxfp4_bias_act(A, a_scales, B, b_scales, bias, C, act="none", alpha: float = 0.0, stream=None):
+    """C = act(A @ B.T + bias), B in MXFP4 (codes and b_scales of its N rows);
+    A in MXFP4 (codes and a_scales), or fp16 / bf16 with a_scales None."""
+    M, N, K, dt = _gemm_mx_args(A, a_scales, B, b_scales, bias, C)
+    rc = lib.gemm_mxfp4_bias_act(_dev(A, "A"), _dev(a_scales, "a_scales"), _dev(B, "B"),
+                                 _dev(b_scales, "b_scales"), _dev(bias, "bias"), _dev(C, "C"), M, N, K, dt,
+                                 _act(act), float(alpha), _stream(stream))
+    _check(rc, "gemm_mxfp4_bias_act")
+    return C
+
+
+def gemm_mxfp4_bias_add_act(A, a_scales, B, b_scales, bias, R, C, act="none", alpha: float = 0.0,
+                            stream=None):
+    """C = act(A @ B.T + bias + R); R like C (may be C itself)."""
+    M, N, K, dt = _gemm_mx_args(A, a_scales, B, b_scales, bias, C)
+    rc = lib.gemm_mxfp4_bias_add_act(_dev(A, "A"), _dev(a_scales, "a_scales"), _dev(B, "B"),
+                                     _dev(b_scales, "b_scales"), _dev(bias, "bias"), _residual(R, C),
+                                     _dev(C, "C"), M, N, K, dt, _act(act), float(alpha), _stream(stream))
+    _check(rc, "gemm_mxfp4_bias_add_act")
+    return C
 
 
 # -- tile configs ------------------------------------------------------------

@@ -30,8 +30,9 @@ ARCH = "gfx950"
 _TYPES = ("f32", "f16", "bf16")
 HIP_SOURCES = ["api.hip", "act_cast.hip", "dispatch.hip"] + [
     f"{op}_{ti}_{to}.hip" for op in ("gemm", "conv") for ti in _TYPES for to in _TYPES] + [
-    f"gemm_i8_{to}.hip" for to in ("f32", "f16", "bf16", "i32")]
-CPP_SOURCES = ["plan.cpp"]
+    f"gemm_i8_{to}.hip" for to in ("f32", "f16", "bf16", "i32")] + [
+    "mx_quant.hip"] + [f"gemm_mx_{ta}.hip" for ta in ("mxfp4", "f16", "bf16")]
+CPP_SOURCES = ["plan.cpp", "plan_mx.cpp"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-I", INCLUDE, "-I", CSRC, "-Wall",
           "-Wno-unused-command-line-argument"]

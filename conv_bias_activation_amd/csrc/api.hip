@@ -12,6 +12,7 @@
 #include "biasact.h"
 #include "launch.hpp"
 #include "launch_kernel.hpp"
+#include "mx_launch.hpp"
 #include "plan.hpp"
 
 using namespace biasact;
@@ -233,6 +234,63 @@ int conv_2k_impl(const void* x, const void* w, const void* bias, const void* r, 
   if (rc) return rc;
   note_two_kernel();
   return launch_second_kernel(p.dto, workspace, y, need / 4u, act, 0.0f, r, stream);
+}
+
+// ---- MXFP4 ------------------------------------------------------------------
+int mx_quant_impl(const void* X, const void* codes, const void* scales, int64_t rows, int64_t K, int k_axis,
+                  uint32_t dtype, bool back, hipStream_t s) {
+  MxQuantPlan p;
+  const int rc = plan_mx_quant(X, codes, scales, rows, K, k_axis, dtype, &p);
+  if (rc || p.empty) return rc;
+  MxQuantArgs a;
+  a.X = X;
+  a.codes = const_cast<void*>(codes);
+  a.scales = const_cast<void*>(scales);
+  a.rows = p.rows;
+  a.K = p.K;
+  a.G = p.G;
+  a.total = p.rows * p.G * 16u;
+  a.div_row = make_fastdiv(p.G * 16u);
+  a.div_tiles = make_fastdiv((p.rows + 63u) / 64u);
+  if (launch_mx_quant(p.dt, a, k_axis == 1, back, s)) return kErrUnsupported;
+  return launch_status();
+}
+
+int gemm_mx_impl(const void* A, const void* As, const void* B, const void* Bs, const void* bias, const void* R,
+                 void* C, int64_t M, int64_t N, int64_t K, uint32_t dtypes, int act, float alpha, hipStream_t s) {
+  MxGemmPlan p;
+  int rc = plan_mx_gemm(A, As, B, Bs, bias, R, C, M, N, K, dtypes, act, &p);
+  if (rc || p.empty) return rc;
+  MxGemmArgs a;
+  a.A = A;
+  a.As = As;
+  a.B = B;
+  a.Bs = Bs;
+  a.bias = bias;
+  a.R = R;
+  a.C = C;
+  a.M = p.M;
+  a.N = p.N;
+  a.K = p.K;
+  a.G = p.G;
+  a.a_bytes = p.a_bytes;
+  a.as_bytes = p.as_bytes;
+  a.b_bytes = p.b_bytes;
+  a.bs_bytes = p.bs_bytes;
+  a.bias_bytes = p.bias_bytes;
+  a.c_bytes = p.c_bytes;
+  a.bias_dt = p.bias_dt;
+  a.act = act;
+  a.alpha = alpha;
+  a.tiles_m = a.tiles_n = 0;       // set with the tile
+  switch (p.dta) {
+    case DT_MXFP4: rc = launch_gemm_mx_mxfp4(p.dto, a, s); break;
+    case DT_F16: rc = launch_gemm_mx_f16(p.dto, a, s); break;
+    case DT_BF16: rc = launch_gemm_mx_bf16(p.dto, a, s); break;
+    default: return kErrUnsupported;
+  }
+  if (rc) return kErrUnsupported;
+  return launch_status();
 }
 
 // ---- the two-kernel GEMM without allocation -------------------------------
@@ -474,6 +532,38 @@ int conv2d_bias_add_act_2k(const void* x, const void* w, const void* bias, const
   if (!r && N > 0) return kErrInvalid;
   return conv_2k_impl(x, w, bias, r, y, N, C, H, W, Co, kh, kw, strides, pads, dilations, dtypes,
                       act, workspace, workspace_bytes, stream);
+}
+
+int mxfp4_packed_size(int64_t rows, int64_t K, size_t* codes_bytes, size_t* scales_bytes) {
+  if (rows < 0 || K < 0 || !codes_bytes || !scales_bytes) return kErrInvalid;
+  if (rows >= (1ll << 31) || K >= (1ll << 31)) return kErrUnsupported;
+  const size_t groups = (size_t)rows * (size_t)((K + 127) / 128);
+  *codes_bytes = groups * 64u;
+  *scales_bytes = groups * 4u;
+  return kOk;
+}
+
+int mxfp4_quantize(const void* X, void* codes, void* scales, int64_t rows, int64_t K, int k_axis, uint32_t dtype,
+                   hipStream_t stream) {
+  return mx_quant_impl(X, codes, scales, rows, K, k_axis, dtype, false, stream);
+}
+
+int mxfp4_dequantize(const void* codes, const void* scales, void* Y, int64_t rows, int64_t K, int k_axis,
+                     uint32_t dtype, hipStream_t stream) {
+  return mx_quant_impl(Y, codes, scales, rows, K, k_axis, dtype, true, stream);
+}
+
+int gemm_mxfp4_bias_act(const void* A, const void* a_scales, const void* B, const void* b_scales, const void* bias,
+                        void* C, int64_t M, int64_t N, int64_t K, uint32_t dtypes, int act, float alpha,
+                        hipStream_t stream) {
+  return gemm_mx_impl(A, a_scales, B, b_scales, bias, nullptr, C, M, N, K, dtypes, act, alpha, stream);
+}
+
+int gemm_mxfp4_bias_add_act(const void* A, const void* a_scales, const void* B, const void* b_scales,
+                            const void* bias, const void* R, void* C, int64_t M, int64_t N, int64_t K,
+                            uint32_t dtypes, int act, float alpha, hipStream_t stream) {
+  if (!R && M > 0 && N > 0) return kErrInvalid;
+  return gemm_mx_impl(A, a_scales, B, b_scales, bias, R, C, M, N, K, dtypes, act, alpha, stream);
 }
 
 int biasact_gemm_path(int64_t M, int64_t N, int64_t K, uint32_t dtypes, int act) {

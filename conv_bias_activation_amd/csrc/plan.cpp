@@ -430,10 +430,12 @@ const char* status_string(int s) {
     case kOk: return "ok";
     case kErrInvalid:
       return "invalid argument (null pointer, negative or empty dimension, bad activation, "
-             "stride/dilation < 1, pad < 0, empty conv output, or workspace too small)";
+             "stride/dilation < 1, pad < 0, empty conv output, workspace too small, or a misaligned or "
+             "unexpected MXFP4 operand)";
     case kErrUnsupported:
       return "unsupported (element types: A = B in {f32, f16, bf16}, bias in {f32, input type}, "
-             "output in {f32, f16, bf16}; conv has no LeakyReLU; every tensor < 2^31 bytes)";
+             "output in {f32, f16, bf16}; conv has no LeakyReLU; MXFP4 products: B in mxfp4, A in "
+             "{mxfp4, f16, bf16}; every tensor < 2^31 bytes)";
     case kErrHip: return "HIP runtime error at launch";
     default: return "unknown status";
   }

@@ -59,6 +59,25 @@ int plan_conv(const void* x, const void* w, const void* bias, const void* y, int
               const int32_t* pads, const int32_t* dilations, uint32_t dtypes, int act,
               ConvPlan* p, const void* r = nullptr);
 
+// MXFP4 operators (plan_mx.cpp); G = ceil(K / 128) groups a row.
+struct MxQuantPlan {
+  int dt;
+  uint32_t rows, K, G;
+  bool empty;                      // nothing to launch
+};
+
+struct MxGemmPlan {
+  int dta, dto, bias_dt;           // bias_dt = -1 without bias
+  uint32_t M, N, K, G;
+  uint32_t a_bytes, as_bytes, b_bytes, bs_bytes, bias_bytes, c_bytes;
+  bool empty;                      // M == 0 or N == 0: nothing to launch
+};
+
+int plan_mx_quant(const void* X, const void* codes, const void* scales, int64_t rows, int64_t K, int k_axis,
+                  uint32_t dtype, MxQuantPlan* p);
+int plan_mx_gemm(const void* A, const void* As, const void* B, const void* Bs, const void* bias, const void* R,
+                 const void* C, int64_t M, int64_t N, int64_t K, uint32_t dtypes, int act, MxGemmPlan* p);
+
 // Output size of conv2d with zero padding (floor rounding); kErrInvalid for
 // bad strides / pads / dilations or an empty output.
 int conv_out_dims(int64_t H, int64_t W, int64_t kh, int64_t kw, const int32_t* strides,

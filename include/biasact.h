@@ -60,6 +60,7 @@ extern "C" {
 #define BA_BF16 2u
 #define BA_I8 3u            /* two's complement int8: GEMM operands only */
 #define BA_I32 4u           /* two's complement int32: bias / output of int8 GEMMs */
+#define BA_MXFP4 5u         /* 4-bit floating point in scaled blocks (below): gemm_mxfp4_* operands only */
 
 /* dtypes argument: one 8-bit code per operand.
  *   a   : A (GEMM) or x (conv)
@@ -198,6 +199,56 @@ int conv2d_bias_add_act_2k(const void* x, const void* w, const void* bias, const
                            int64_t kw, const int32_t strides[2], const int32_t pads[4],
                            const int32_t dilations[2], uint32_t dtypes, int act, void* workspace,
                            size_t workspace_bytes, hipStream_t stream);
+
+/* MXFP4: 4-bit floating point in blocks of 32 values with a shared scale.
+ * A value is a code (1 sign, 2 exponent, 1 mantissa bit: 0, 0.5, 1, 1.5, 2,
+ * 3, 4, 6 and their negatives) times its block's scale 2^(b - 127), b one
+ * byte; b = 255 is NaN.  Blocks run along the reduction index k.  An operand
+ * of `rows` rows of K values is two packed arrays:
+ *   codes  [rows, 64 * ceil(K / 128)] bytes, k even in a byte's low four bits,
+ *   scales [rows,  4 * ceil(K / 128)] bytes,
+ * i.e. each row is padded to whole groups of 128 values; the padding must be
+ * zero codes (mxfp4_quantize writes it so, with scale bytes of zero).  codes
+ * must be 16-byte and scales 4-byte aligned (BA_ERR_INVALID otherwise).
+ *
+ * mxfp4_packed_size: bytes of the two arrays (host pointers). */
+int mxfp4_packed_size(int64_t rows, int64_t K, size_t* codes_bytes, size_t* scales_bytes);
+
+/* X -> codes, scales.  X is fp32, fp16 or bf16 (dtype: one BA_* code), packed
+ * [rows, K] with k_axis = 1 (activations), or [K, rows] with k_axis = 0 (a
+ * weight in gemm_bias_act's B layout: each column becomes one row of codes).
+ * Per block: e = floor(log2 max|x|) - 2, clamped to [-127, 127]; scale byte
+ * e + 127; each code is x / 2^e rounded to the nearest magnitude, ties to the
+ * even code, above 6 to 6, with x's sign.  A block of zeros takes scale byte
+ * 0; a block that holds an infinity or a NaN takes scale byte 255 and zero
+ * codes, and reads back as NaN.  rows, K >= 0 (either 0: nothing to do). */
+int mxfp4_quantize(const void* X, void* codes, void* scales, int64_t rows, int64_t K, int k_axis,
+                   uint32_t dtype, hipStream_t stream);
+
+/* codes, scales -> Y, laid out and typed like X above: each value's code times
+ * its scale, rounded to nearest even where Y's type cannot hold it (fp32 holds
+ * every value up to its range; bf16 too; fp16 overflows to infinity). */
+int mxfp4_dequantize(const void* codes, const void* scales, void* Y, int64_t rows, int64_t K,
+                     int k_axis, uint32_t dtype, hipStream_t stream);
+
+/* C[M,N] = act(A[M,K] . B[N,K]^T + bias[N])  and  act(A . B^T + bias + R).
+ * B is an MXFP4 operand of N rows (dtypes' b = BA_MXFP4).  A is an MXFP4
+ * operand of M rows with its a_scales (dtypes' a = BA_MXFP4), or a packed
+ * fp16 / bf16 [M,K] with a_scales NULL.  bias and out: fp32, fp16 or bf16
+ * each; R has C's type and shape and may be C itself.  The products are exact
+ * (a 16-bit A's values are not rounded further), the sum, bias, residual and
+ * activation run in fp32 with one rounding to C; the sum's order depends on
+ * the sizes only, so equal calls give equal bits.  M, N, K >= 0 (M or N == 0:
+ * nothing to do; K == 0: C = act(bias (+ R))).  Checks, limits and return
+ * codes otherwise as gemm_bias_act / gemm_bias_add_act; the forced tile
+ * configuration does not apply. */
+int gemm_mxfp4_bias_act(const void* A, const void* a_scales, const void* B, const void* b_scales,
+                        const void* bias, void* C, int64_t M, int64_t N, int64_t K,
+                        uint32_t dtypes, int act, float alpha, hipStream_t stream);
+int gemm_mxfp4_bias_add_act(const void* A, const void* a_scales, const void* B,
+                            const void* b_scales, const void* bias, const void* R, void* C,
+                            int64_t M, int64_t N, int64_t K, uint32_t dtypes, int act, float alpha,
+                            hipStream_t stream);
 
 /* Fused or two-kernel path, chosen per problem.  The pages decide at run
  * time whether to fuse: ops-nn (mlqm.cn/news/1824, sections
