@@ -187,15 +187,34 @@ def _dev(t, name):
         raise ValueError(f"{name} must be a device tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous (packed, row-major)")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
+
+
+def _current_stream():
+    """() -> handle of the current device's current stream.  torch's public
+    call builds a Stream object each time (2.6 us of host time, as much as a
+    launch); the raw form that its own generated code uses takes 0.1 us."""
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    dev = getattr(torch._C, "_cuda_getDevice", None)
+    if raw is None or dev is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    return lambda: raw(dev())
+
+
+_current = None      # set on first use: torch's device state must exist by then
 
 
 def _stream(stream):
+    global _current
     if stream is None:
-        return ctypes.c_void_p(_torch().cuda.current_stream().cuda_stream)
+        if _current is None:
+            _torch().cuda.current_stream()
+            _current = _current_stream()
+        return _current()
     if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
-    return ctypes.c_void_p(stream.cuda_stream)
+        return stream
+    return stream.cuda_stream
 
 
 def _i32x(vals: Sequence[int], n: int, name: str):
@@ -480,27 +499,28 @@ def mxfp4_shapes(rows: int, K: int):
 
 
 def _packed(codes, scales, name):
-    """Groups of 128 values per row of an MXFP4 operand, checked."""
+    """(rows, groups of 128 values per row) of an MXFP4 operand, checked."""
     u8 = _torch().uint8
     if codes.dtype != u8 or scales.dtype != u8:
         raise ValueError(f"{name}: codes and scales must be uint8")
-    if codes.dim() != 2 or scales.dim() != 2:
-        raise ValueError(f"{name}: codes and scales must be 2-D")
-    g = scales.shape[1] // 4
-    if scales.shape[1] != 4 * g or tuple(codes.shape) != (scales.shape[0], 64 * g):
+    cs, ss = codes.shape, scales.shape
+    if len(cs) != 2 or len(ss) != 2 or cs[0] != ss[0] or cs[1] != 16 * ss[1] or ss[1] % 4:
         raise ValueError(f"{name}: codes must be [rows, 64 g] and scales [rows, 4 g], got "
-                         f"{tuple(codes.shape)} and {tuple(scales.shape)}")
-    return g
+                         f"{tuple(cs)} and {tuple(ss)}")
+    return ss[0], ss[1] >> 2
 
 
 def _mx_quant_args(X, codes, scales, axis, name):
-    if X.dim() != 2:
+    shape = X.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must be 2-D")
-    if axis not in (0, 1):
+    if axis == 1:
+        rows, K = shape
+    elif axis == 0:
+        K, rows = shape
+    else:
         raise ValueError("axis must be 0 or 1")
-    rows, K = X.shape if axis == 1 else (X.shape[1], X.shape[0])
-    _packed(codes, scales, "mxfp4")
-    if (tuple(codes.shape), tuple(scales.shape)) != mxfp4_shapes(rows, K):
+    if _packed(codes, scales, "mxfp4") != (rows, (K + 127) >> 7):
         raise ValueError(f"codes and scales must be {mxfp4_shapes(rows, K)}, got "
                          f"{tuple(codes.shape)} and {tuple(scales.shape)}")
     return rows, K, DTYPE_CODES[_tname(X)]
@@ -528,15 +548,15 @@ def mxfp4_dequantize(codes, scales, Y, axis: int = 1, stream=None):
 
 
 def _gemm_mx_args(A, a_scales, B, b_scales, bias, C):
-    g = _packed(B, b_scales, "B")
-    if A.dim() != 2 or C.dim() != 2:
-        raise ValueError("A and C must be 2-D")
-    M, N = A.shape[0], B.shape[0]
+    N, g = _packed(B, b_scales, "B")
     if a_scales is not None:
-        K, ta = 128 * _packed(A, a_scales, "A"), "mxfp4"
+        M, ga = _packed(A, a_scales, "A")
+        K, ta = 128 * ga, "mxfp4"
+    elif A.dim() == 2:
+        (M, K), ta = A.shape, _tname(A)
     else:
-        K, ta = A.shape[1], _tname(A)
-    if -(-K // 128) != g or tuple(C.shape) != (M, N):
+        raise ValueError("A must be 2-D")
+    if (K + 127) >> 7 != g or C.shape != (M, N):
         raise ValueError(f"shape mismatch: A{tuple(A.shape)} B{tuple(B.shape)} C{tuple(C.shape)}")
     if bias is not None and bias.numel() != N:
         raise ValueError(f"bias must have N = {N} elements")

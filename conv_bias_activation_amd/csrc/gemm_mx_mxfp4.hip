@@ -1,5 +1,5 @@
 // gemm_mx_mxfp4.hip — fused product with an MXFP4 B + bias + activation, A in mxfp4.
-#include "gemm_mx.hpp"
+#include "gemm_mx_launch.hpp"
 
 namespace biasact {
 int launch_gemm_mx_mxfp4(int dto, const MxGemmArgs& a, hipStream_t s) {
