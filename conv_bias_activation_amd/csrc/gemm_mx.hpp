@@ -3,28 +3,27 @@
 // B in MXFP4 (mx_args.hpp), A in MXFP4, fp16 or bf16.
 //
 // Streaming kernel.  A wave holds a block of 16 NB rows of B (n) by 16 MB rows
-// of A (m) and walks k; the workgroup's waves take turns along k and add their
+// of A (m) and walks its part of k; the workgroup's waves split k and add their
 // sums through LDS at the end, in wave order, so every result has one fixed
-// order of additions.  Operands go from global memory straight to registers;
-// a piece's registers are loaded anew, for a later group, as soon as its
-// matrix instructions are issued.
+// order of additions.
 //
-// k advances by groups of 128.  Lane L (row r = L % 16, g = L / 16) loads 16
-// bytes of codes, block g of its row's group, so one load covers 64
-// consecutive bytes of each of 16 rows, and the group's four scale bytes as
-// one word.
-//   MXFP4 A: v_mfma_scale_f32_16x16x128 takes the blocks as they lie, each lane
-//     with its own scale (byte g of the word, shifted down).
-//   16-bit A: four 4x4 transpositions across the lanes of a row (two half-wave
-//     and two row swaps) turn the block per lane into dword g of each of the
-//     four blocks: matrix instruction c then covers the 32 k of block c, lane g
-//     the eight from 8 g on, and A's loads too cover 64 consecutive bytes a row.
-//     The codes become bf16 values with their scale (exact: two significant
-//     bits and bf16's fp32 exponent range) for v_mfma_f32_16x16x32_bf16.
-//   fp16 A: while every scale of a group lies in 2^-13 .. 2^13 its values are
-//     normal fp16 numbers and go to v_mfma_f32_16x16x32_f16.  Otherwise A's
-//     values are split into bf16 parts x = hi + lo, exactly (11 significant
-//     bits into 8 + 3), with an instruction for each.
+// k advances by groups of 128.  Four neighbouring lanes load 64 consecutive
+// bytes of one row: a load then touches 16 cache lines, where the layout of
+// the matrix instructions (lanes r, r + 16, r + 32, r + 48 share row r) would
+// touch 64, and the address unit takes one a cycle.  Each wave turns that into
+// the instruction's layout through LDS of its own, a row's 16-byte chunk c at
+// slot c ^ ((row >> 2) & 3) so that neither side meets a bank twice; a wave's
+// LDS operations run in order, so this needs no barrier.  A register is loaded
+// anew, for the group that is UN further, as soon as it has gone to LDS.  Scale
+// words come for four groups at a time, one row a lane.
+//   MXFP4 A: v_mfma_scale_f32_16x16x128, lane (r, g) with block g of row r and
+//     its scale (byte g of the word, shifted down).
+//   16-bit A: v_mfma_f32_16x16x32 c covers block c, lane (r, g) the eight k from
+//     8 g on.  For bf16 the codes become bf16 values with their scale, which is
+//     exact (two significant bits and bf16's fp32 exponent range).  For fp16
+//     they become fp16 values with their scale while every scale in sight lies
+//     in 2^-13 .. 2^13 (0.5 and 6 times it are normal fp16 numbers); else each
+//     block's products are summed unscaled and scaled in fp32.
 #pragma once
 
 #include "epilogue.hpp"
@@ -47,26 +46,6 @@ __device__ __forceinline__ f32x4 mfma_mx(u32x4 a, u32x4 b, f32x4 acc, uint32_t s
   const i32x8 x = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
   const i32x8 y = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, acc, 4, 4, 0, (int)sa, 0, (int)sb);
-}
-
-// Register c of lane (r, g) becomes register g of lane (r, c).
-__device__ __forceinline__ void transpose_groups(u32x4& v) {
-  auto swap32 = [](uint32_t& a, uint32_t& b) {        // upper half of a <-> lower half of b
-    const auto s = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-    a = s[0];
-    b = s[1];
-  };
-  auto swap16 = [](uint32_t& a, uint32_t& b) {        // odd 16-lane rows of a <-> even rows of b
-    const auto s = __builtin_amdgcn_permlane16_swap(a, b, false, false);
-    a = s[0];
-    b = s[1];
-  };
-  uint32_t d0 = v.x, d1 = v.y, d2 = v.z, d3 = v.w;
-  swap32(d0, d2);
-  swap32(d1, d3);
-  swap16(d0, d1);
-  swap16(d2, d3);
-  v = u32x4{d0, d1, d2, d3};
 }
 
 // eight codes -> bf16 with their scale (exponent field of s)
@@ -99,20 +78,14 @@ __device__ __forceinline__ f32x4 mfma_f16(u32x4 a, u32x4 b, f32x4 acc) {
                                                 0, 0);
 }
 
-// Two fp16 values as bf16 pairs: hi = x rounded to 8 significant bits, lo the
-// rest.  An infinity keeps its hi part alone (the rest would be NaN).
-__device__ __forceinline__ void split_f16(uint32_t w, uint32_t& hi, uint32_t& lo) {
-  uint32_t h[2], l[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const float x = widen<DT_F16>((w >> (16 * e)) & 0xffffu);
-    h[e] = narrow<DT_BF16>(x);
-    const float d = x - widen<DT_BF16>(h[e]);
-    l[e] = __builtin_fabsf(x) == __builtin_inff() ? 0u : narrow<DT_BF16>(d);
-  }
-  hi = h[0] | (h[1] << 16);
-  lo = l[0] | (l[1] << 16);
+// 2^(b - 127), NaN for 255, as fp32
+__device__ __forceinline__ float scale_value(uint32_t b) {
+  return __uint_as_float(b == 255u ? 0x7fc00000u : b == 0u ? 0x00400000u : b << 23);
 }
+
+// Orders a wave's LDS accesses before and after (the hardware runs them in
+// order; this keeps the compiler from exchanging them).
+__device__ __forceinline__ void lds_order() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
 // Eight 16-bit values; p need only be aligned for one.
 __device__ __forceinline__ u32x4 load_x8(const uint8_t* p) {
@@ -145,56 +118,83 @@ __device__ __forceinline__ float act(float z, float alpha) {
 template <int DTA, int DTO, int NB, int MB, int NW, int UN>
 __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxGemmArgs a) {
   constexpr int TN = 16 * NB, TM = 16 * MB;
-  // partial sums of one wave, [m][n] with n contiguous; 4 floats of padding a
-  // row keep the rows that one store instruction covers on different banks
+  // Per wave: one group of B, one piece of A (1 KB per 16 rows), four groups'
+  // scale words; at the end the waves' sums, [m][n] with n contiguous and 4
+  // floats of padding a row, which keeps the rows of one access on different
+  // banks.
   constexpr int LDR = TN + 4;
-  __shared__ __attribute__((aligned(16))) float red[NW][TM][LDR];
+  constexpr int SROWS = TN + (DTA == DT_MXFP4 ? TM : 0);
+  constexpr int W_AT = 0, X_AT = NB * 1024, S_AT = X_AT + MB * 1024, WAVE = S_AT + SROWS * 16;
+  constexpr int SUMS = TM * LDR * 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[NW * (WAVE > SUMS ? WAVE : SUMS)];
 
   // neighbouring workgroups of an XCD share rows of B
   const uint32_t t = xcd_contiguous(blockIdx.x, gridDim.x);
   const uint32_t tn = t / a.tiles_m, tm = t - tn * a.tiles_m;
   const uint32_t n0 = tn * TN, m0 = tm * TM;
-  const int lane = threadIdx.x & 63;
+  const uint32_t lane = threadIdx.x & 63;
   const uint32_t w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t r = lane & 15, g = lane >> 4;
+  const uint32_t r = lane & 15, g = lane >> 4;        // the matrix instructions' lane layout
+  const uint32_t lr = lane >> 2, lc = lane & 3;       // the loads': row, 16-byte chunk
+  uint8_t* const my = smem + w * WAVE;
+  const uint32_t put = lr * 64u + ((lc ^ (lr >> 2)) << 4);            // a loaded chunk's place
+  const uint32_t get = r * 64u, sw = r >> 2;                          // row r's chunk c: get + ((c ^ sw) << 4)
 
   // Rows past the end are not stored: those of packed operands read as zeros or
   // as whatever row their offset wraps to, those of a 16-bit A repeat its last.
   const __amdgpu_buffer_rsrc_t rb = make_rsrc(a.B, a.b_bytes), rbs = make_rsrc(a.Bs, a.bs_bytes);
   const __amdgpu_buffer_rsrc_t ra = make_rsrc(a.A, a.a_bytes), ras = make_rsrc(a.As, a.as_bytes);
   const uint8_t* A = static_cast<const uint8_t*>(a.A);
-  const uint32_t wrow = (n0 + r) * a.G, mrow = (m0 + r) * a.G;
+  const uint32_t wrow = (n0 + lr) * a.G, mrow = (m0 + lr) * a.G;
   uint32_t xrow[MB];
 #pragma unroll
-  for (int j = 0; j < MB; ++j) xrow[j] = min(m0 + 16 * j + r, a.M - 1) * a.K;
+  for (int j = 0; j < MB; ++j) xrow[j] = min(m0 + 16 * j + lr, a.M - 1) * a.K;
 
-  // UN groups under way: codes and scales of B, 16-byte pieces (and scales) of A
+  // this wave's groups of k: q0 .. q1 - 1
+  const uint32_t per = (a.G + NW - 1) / NW, q0 = min(w * per, a.G), q1 = min(q0 + per, a.G);
+
+  // UN groups under way: codes of B, 16-byte pieces of A
   constexpr int XC = DTA == DT_MXFP4 ? 1 : 4;
   u32x4 wc[UN][NB], xc[UN][MB][XC];
-  uint32_t ws[UN][NB], xs[UN][MB];
   auto load_w = [&](int u, uint32_t q) {
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const uint32_t at = wrow + (16u * i * a.G + q);
-      wc[u][i] = ld_b128(rb, at * 64u + 16u * g);
-      ws[u][i] = ld_b32(rbs, at * 4u);
-    }
+    for (int i = 0; i < NB; ++i) wc[u][i] = ld_b128(rb, (wrow + (16u * i * a.G + q)) * 64u + 16u * lc);
   };
-  // Piece c of A: values 128 q + 32 c + 8 g .. + 7 of each row; where that runs
+  // Piece c of A: values 128 q + 32 c + 8 lc .. + 7 of each row; where that runs
   // past K (>= 8 for a 16-bit A), the row's last eight, shifted down on use.
   auto load_x = [&](int u, int c, uint32_t q) {
     if constexpr (DTA == DT_MXFP4) {
 #pragma unroll
-      for (int j = 0; j < MB; ++j) {
-        const uint32_t at = mrow + (16u * j * a.G + q);
-        xc[u][j][0] = ld_b128(ra, at * 64u + 16u * g);
-        xs[u][j] = ld_b32(ras, at * 4u);
-      }
+      for (int j = 0; j < MB; ++j) xc[u][j][0] = ld_b128(ra, (mrow + (16u * j * a.G + q)) * 64u + 16u * lc);
     } else {
-      const uint32_t k = min(q * 128u + c * 32u + g * 8u, a.K - 8u);
+      const uint32_t k = min(q * 128u + c * 32u + lc * 8u, a.K - 8u);
 #pragma unroll
       for (int j = 0; j < MB; ++j) xc[u][j][c] = mx::load_x8(A + (size_t)((xrow[j] + k) * 2u));
     }
+  };
+  // Scale words of groups q .. q + 3 (none past the row's end): row n0 + lane of
+  // B for the first 16 NB lanes, and row m0 + lane of an MXFP4 A.
+  auto load_s = [&](__amdgpu_buffer_rsrc_t rs, uint32_t row, uint32_t q) {
+    u32x4 v = {0, 0, 0, 0};
+    const uint32_t at = (row * a.G + q) * 4u;
+    if (q + 4 <= a.G) {                                // uniform
+      v = ld_b128(rs, at);
+    } else {
+#pragma unroll
+      for (uint32_t e = 0; e < 3; ++e)
+        if (q + e < a.G) v[e] = ld_b32(rs, at + e * 4u);
+    }
+    return v;
+  };
+  u32x4 sb = {0, 0, 0, 0}, sa = {0, 0, 0, 0};
+  auto load_scales = [&](uint32_t q) {
+    sb = load_s(rbs, n0 + min(lane, TN - 1u), q);
+    if constexpr (DTA == DT_MXFP4) sa = load_s(ras, m0 + min(lane, TM - 1u), q);
+  };
+  auto put_scales = [&] {
+    if (lane < TN) *reinterpret_cast<u32x4*>(my + S_AT + lane * 16u) = sb;
+    if constexpr (DTA == DT_MXFP4)
+      if (lane < TM) *reinterpret_cast<u32x4*>(my + S_AT + (TN + lane) * 16u) = sa;
   };
 
   f32x4 acc[NB][MB];
@@ -203,99 +203,110 @@ __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxGemmArgs a) {
 #pragma unroll
     for (int j = 0; j < MB; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // Adds group q's products from slot u and loads group q + UN NW into it.
+  // Adds group q's products from slot u and loads group q + UN into it.
   auto multiply = [&](int u, uint32_t q) {
-    const uint32_t qn = q + UN * NW;
-    const bool more = qn < a.G;                        // uniform
+    const bool more = q + UN < q1;                     // uniform
+    const uint32_t word = (q - q0) & 3u;               // of the scale words at hand
+    mx::lds_order();
+    if (word == 0) {
+      put_scales();
+      if (q + 4 < q1) load_scales(q + 4);
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i) *reinterpret_cast<u32x4*>(my + W_AT + i * 1024 + put) = wc[u][i];
+    if (more) load_w(u, q + UN);
     if constexpr (DTA == DT_MXFP4) {
+#pragma unroll
+      for (int j = 0; j < MB; ++j) *reinterpret_cast<u32x4*>(my + X_AT + j * 1024 + put) = xc[u][j][0];
+      if (more) load_x(u, 0, q + UN);
+      mx::lds_order();
+      u32x4 xf[MB];
       uint32_t sx[MB];
 #pragma unroll
-      for (int j = 0; j < MB; ++j) sx[j] = xs[u][j] >> (8 * g);
+      for (int j = 0; j < MB; ++j) {
+        xf[j] = *reinterpret_cast<const u32x4*>(my + X_AT + j * 1024 + get + ((g ^ sw) << 4));
+        sx[j] = *reinterpret_cast<const uint32_t*>(my + S_AT + (TN + 16 * j + r) * 16 + word * 4) >> (8 * g);
+      }
 #pragma unroll
-      for (int i = 0; i < NB; ++i)
+      for (int i = 0; i < NB; ++i) {
+        const u32x4 wf = *reinterpret_cast<const u32x4*>(my + W_AT + i * 1024 + get + ((g ^ sw) << 4));
+        const uint32_t ws = *reinterpret_cast<const uint32_t*>(my + S_AT + (16 * i + r) * 16 + word * 4) >> (8 * g);
 #pragma unroll
-        for (int j = 0; j < MB; ++j)
-          acc[i][j] = mx::mfma_mx(wc[u][i], xc[u][j][0], acc[i][j], ws[u][i] >> (8 * g), sx[j]);
-      if (more) {
-        load_w(u, qn);
-        load_x(u, 0, qn);
+        for (int j = 0; j < MB; ++j) acc[i][j] = mx::mfma_mx(wf, xf[j], acc[i][j], ws, sx[j]);
       }
     } else {
-      u32x4 wv[NB];
-      uint32_t sw[NB];
-      bool normal = DTA == DT_F16;
+      mx::lds_order();
+      uint32_t ws[NB];                                 // the four blocks' scale bytes of row 16 i + r
+      bool normal = true;
 #pragma unroll
       for (int i = 0; i < NB; ++i) {
-        wv[i] = wc[u][i];
-        sw[i] = ws[u][i];
-      }
-      // (the widest fp16 block has no registers for the next codes beside these:
-      // it loads them last)
-      constexpr bool LATE = DTA == DT_F16 && NB * MB == 16;
-      if (more && !LATE) load_w(u, qn);
+        ws[i] = *reinterpret_cast<const uint32_t*>(my + S_AT + (16 * i + r) * 16 + word * 4);
+        if constexpr (DTA == DT_F16)
 #pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        mx::transpose_groups(wv[i]);
-        if constexpr (DTA == DT_F16)                   // 2^-13 .. 2^13: 0.5 and 6 times it are normal in fp16
-#pragma unroll
-          for (int c = 0; c < 4; ++c) normal = normal && ((sw[i] >> (8 * c)) & 255u) - 114u <= 26u;
+          for (int c = 0; c < 4; ++c)                  // (padding past K holds zeros, whatever its scale)
+            normal = normal && (((ws[i] >> (8 * c)) & 255u) - 114u <= 26u || q * 128u + c * 32u >= a.K);
       }
       if constexpr (DTA == DT_F16) normal = __all(normal);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         if ((q + 1) * 128u > a.K) {                    // uniform: the row ends in this group
-          const uint32_t k = q * 128u + c * 32u + g * 8u;
+          const uint32_t k = q * 128u + c * 32u + lc * 8u;
 #pragma unroll
           for (int j = 0; j < MB; ++j) xc[u][j][c] = mx::shift_x8(xc[u][j][c], k - min(k, a.K - 8u));
         }
-        auto scale = [&](int i) { return __uint_as_float(((sw[i] >> (8 * c)) & 255u) << 23); };
+        mx::lds_order();
+#pragma unroll
+        for (int j = 0; j < MB; ++j) *reinterpret_cast<u32x4*>(my + X_AT + j * 1024 + put) = xc[u][j][c];
+        if (more) load_x(u, c, q + UN);
+        mx::lds_order();
+        u32x4 xf[MB];
+        uint32_t wf[NB];                               // codes of the eight k from 8 g on
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+          wf[i] = *reinterpret_cast<const uint32_t*>(my + W_AT + i * 1024 + get + ((c ^ sw) << 4) + 4 * g);
+#pragma unroll
+        for (int j = 0; j < MB; ++j)
+          xf[j] = *reinterpret_cast<const u32x4*>(my + X_AT + j * 1024 + get + ((g ^ sw) << 4));
+        auto field = [&](int i) { return __uint_as_float(((ws[i] >> (8 * c)) & 255u) << 23); };
         if constexpr (DTA == DT_BF16) {
 #pragma unroll
           for (int i = 0; i < NB; ++i) {
-            const u32x4 v = mx::decode_bf16(wv[i][c], scale(i));
+            const u32x4 v = mx::decode_bf16(wf[i], field(i));
 #pragma unroll
-            for (int j = 0; j < MB; ++j) acc[i][j] = mx::mfma_bf16(v, xc[u][j][c], acc[i][j]);
+            for (int j = 0; j < MB; ++j) acc[i][j] = mx::mfma_bf16(v, xf[j], acc[i][j]);
           }
         } else if (normal) {
 #pragma unroll
           for (int i = 0; i < NB; ++i) {
-            const u32x4 v = mx::decode_f16(wv[i][c], scale(i));
+            const u32x4 v = mx::decode_f16(wf[i], field(i));
 #pragma unroll
-            for (int j = 0; j < MB; ++j) acc[i][j] = mx::mfma_f16(v, xc[u][j][c], acc[i][j]);
+            for (int j = 0; j < MB; ++j) acc[i][j] = mx::mfma_f16(v, xf[j], acc[i][j]);
           }
         } else {
 #pragma unroll
-          for (int j = 0; j < MB; ++j) {
-            __builtin_amdgcn_sched_barrier(0);         // one row block's parts at a time: there are no more registers
-            u32x4 hi, lo;
+          for (int i = 0; i < NB; ++i) {
+            const u32x4 v = mx::decode_f16(wf[i], 1.0f);
+            float s[4];                                // of the sums' rows, 16 i + 4 g + e
 #pragma unroll
-            for (int d = 0; d < 4; ++d) {
-              uint32_t h, l;
-              mx::split_f16(xc[u][j][c][d], h, l);
-              hi[d] = h;
-              lo[d] = l;
-            }
+            for (int e = 0; e < 4; ++e)
+              s[e] = mx::scale_value(my[S_AT + (16 * i + 4 * g + e) * 16 + word * 4 + c]);
 #pragma unroll
-            for (int i = 0; i < NB; ++i) {
-              uint32_t codes = wv[i][c];
-              asm volatile("" : "+v"(codes));          // decoded anew for each j, not kept: registers again
-              const u32x4 v = mx::decode_bf16(codes, scale(i));
-              acc[i][j] = mx::mfma_bf16(v, hi, acc[i][j]);
-              acc[i][j] = mx::mfma_bf16(v, lo, acc[i][j]);
+            for (int j = 0; j < MB; ++j) {
+              const f32x4 z = mx::mfma_f16(v, xf[j], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(z[e], s[e], acc[i][j][e]);
             }
           }
         }
-        if (more) load_x(u, c, qn);
       }
-      if (more && LATE) load_w(u, qn);
     }
   };
 
   // ---- the first groups of this wave -----------------------------------------------
-  const uint32_t q0 = UN * w;
+  if (q0 < q1) load_scales(q0);
 #pragma unroll
   for (int u = 0; u < UN; ++u)
-    if (q0 + u < a.G) {
+    if (q0 + u < q1) {
       load_w(u, q0 + u);
 #pragma unroll
       for (int c = 0; c < XC; ++c) load_x(u, c, q0 + u);
@@ -332,18 +343,22 @@ __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxGemmArgs a) {
   }
 
   // ---- main loop -------------------------------------------------------------------
-  for (uint32_t q = q0; q < a.G; q += UN * NW) {
+  for (uint32_t q = q0; q < q1; q += UN) {
 #pragma unroll
     for (int u = 0; u < UN; ++u)
-      if (q + u < a.G) multiply(u, q + u);
+      if (q + u < q1) multiply(u, q + u);
   }
 
   // ---- sums of the waves, epilogue ---------------------------------------------------
   // accumulator register e of lane (r, g): n = 16 i + 4 g + e, m = 16 j + r
+  __syncthreads();                                     // the sums go over every wave's operands
+  auto sum = [&](uint32_t v, uint32_t ml, uint32_t nl) {
+    return reinterpret_cast<f32x4*>(smem + v * SUMS + (ml * LDR + nl) * 4u);
+  };
 #pragma unroll
   for (int i = 0; i < NB; ++i)
 #pragma unroll
-    for (int j = 0; j < MB; ++j) *reinterpret_cast<f32x4*>(&red[w][16 * j + r][16 * i + 4 * g]) = acc[i][j];
+    for (int j = 0; j < MB; ++j) *sum(w, 16 * j + r, 16 * i + 4 * g) = acc[i][j];
   __syncthreads();
   with_act(a.act, [&](auto act_c) __attribute__((always_inline)) {
     constexpr int ACT = decltype(act_c)::value;
@@ -351,9 +366,9 @@ __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxGemmArgs a) {
     for (int p = 0; p < P; ++p) {
       if (at[p] == kOOB) continue;
       const uint32_t o = threadIdx.x + 64 * NW * p, ml = o / (TN / 4), nl = (o - ml * (TN / 4)) * 4;
-      f32x4 z = *reinterpret_cast<const f32x4*>(&red[0][ml][nl]);
+      f32x4 z = *sum(0, ml, nl);
 #pragma unroll
-      for (int v = 1; v < NW; ++v) z += *reinterpret_cast<const f32x4*>(&red[v][ml][nl]);
+      for (int v = 1; v < NW; ++v) z += *sum(v, ml, nl);
       float y[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) y[e] = mx::act<ACT, DTO>(z[e] + add[p][e], a.alpha);
@@ -399,7 +414,7 @@ inline void launch_mx_short(const MxGemmArgs& a, hipStream_t s) {
 template <int DTA, int DTO, int NB, int MB, int NW>
 inline void launch_mx_stream(MxGemmArgs a, hipStream_t s) {
   // as many groups under way as leave room for the sums and the current one
-  constexpr int GROUP = 5 * NB + (DTA == DT_MXFP4 ? 5 : 16) * MB, LEFT = 150 - 4 * NB * MB;
+  constexpr int GROUP = 4 * NB + (DTA == DT_MXFP4 ? 4 : 16) * MB, LEFT = 150 - 4 * NB * MB;
   constexpr int UN = 4 * GROUP <= LEFT ? 4 : 2 * GROUP <= LEFT ? 2 : 1;
   a.tiles_n = (a.N + 16 * NB - 1) / (16 * NB);
   a.tiles_m = (a.M + 16 * MB - 1) / (16 * MB);

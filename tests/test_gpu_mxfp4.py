@@ -204,7 +204,8 @@ def run_case(ba, M, N, K, kind, out, act="none", bias_dt="f32", residual=False, 
 
 SIZES = [(1, 1, 1), (1, 16, 32), (1, 4096, 512), (2, 17, 33), (7, 250, 4100), (16, 64, 128), (17, 65, 129), (33, 130, 500),
          (48, 96, 1024), (64, 64, 512), (65, 1001, 1503), (128, 256, 1024), (256, 128, 640), (300, 520, 2050),
-         (512, 512, 256), (1000, 72, 96)]
+         (512, 512, 256), (1000, 72, 96), (1, 300, 9000), (3, 5, 7), (40, 64, 8), (2800, 2900, 130), (2049, 4100, 520),
+         (3000, 2816, 1800)]
 
 
 @pytest.mark.parametrize("kind", ["mxfp4", "bf16", "f16"])
@@ -287,7 +288,7 @@ def test_rest_of_a_row_does_not_reach_the_next(ba, kind):
 
 @pytest.mark.parametrize("kind,lo,hi,x", [("mxfp4", 20, 24, 1.0), ("mxfp4", 230, 234, 1.0), ("bf16", 2, 6, 1e30),
                                           ("bf16", 236, 240, 1e-30), ("f16", 60, 64, 6e4), ("f16", 150, 154, 6e-8),
-                                          ("f16", 100, 145, 1.0)])
+                                          ("f16", 100, 145, 1.0), ("f16", 118, 128, 6e-8), ("f16", 115, 139, 1.0)])
 def test_scales_far_from_one(ba, kind, lo, hi, x):
     rng = np.random.default_rng(lo)
     M, N, K = 20, 48, 300
