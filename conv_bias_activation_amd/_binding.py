@@ -150,11 +150,12 @@ def dtypes_code(a: str, b: str, bias: Optional[str], out: str) -> int:
 
 
 def _act(act) -> int:
+    code = ACT_CODES.get(act)
+    if code is not None:
+        return code
     if isinstance(act, int):
         return act
-    if act not in ACT_CODES:
-        raise ValueError(f"unknown activation {act!r}; supported: {sorted(ACT_CODES)}")
-    return ACT_CODES[act]
+    raise ValueError(f"unknown activation {act!r}; supported: {sorted(ACT_CODES)}")
 
 
 # -- torch marshalling ------------------------------------------------------
@@ -183,11 +184,11 @@ def _tname(t) -> str:
 def _dev(t, name):
     if t is None:
         return None
+    if t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous (packed, row-major)")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous (packed, row-major)")
 
 
 def _current_stream():
@@ -498,16 +499,22 @@ def mxfp4_shapes(rows: int, K: int):
     return (int(rows), 64 * g), (int(rows), 4 * g)
 
 
+_U8 = None           # torch.uint8, set on first use
+
+
 def _packed(codes, scales, name):
     """(rows, groups of 128 values per row) of an MXFP4 operand, checked."""
-    u8 = _torch().uint8
-    if codes.dtype != u8 or scales.dtype != u8:
+    global _U8
+    if _U8 is None:
+        _U8 = _torch().uint8
+    shape = scales.shape
+    if (len(shape) == 2 and codes.shape == (shape[0], 16 * shape[1]) and not shape[1] & 3
+            and codes.dtype is _U8 and scales.dtype is _U8):
+        return shape[0], shape[1] >> 2
+    if codes.dtype is not _U8 or scales.dtype is not _U8:
         raise ValueError(f"{name}: codes and scales must be uint8")
-    cs, ss = codes.shape, scales.shape
-    if len(cs) != 2 or len(ss) != 2 or cs[0] != ss[0] or cs[1] != 16 * ss[1] or ss[1] % 4:
-        raise ValueError(f"{name}: codes must be [rows, 64 g] and scales [rows, 4 g], got "
-                         f"{tuple(cs)} and {tuple(ss)}")
-    return ss[0], ss[1] >> 2
+    raise ValueError(f"{name}: codes must be [rows, 64 g] and scales [rows, 4 g], got "
+                     f"{tuple(codes.shape)} and {tuple(shape)}")
 
 
 def _mx_quant_args(X, codes, scales, axis, name):
@@ -533,7 +540,8 @@ def mxfp4_quantize(X, codes, scales, axis: int = 1, stream=None):
     rows, K, dt = _mx_quant_args(X, codes, scales, axis, "X")
     rc = lib.mxfp4_quantize(_dev(X, "X"), _dev(codes, "codes"), _dev(scales, "scales"), rows, K, axis,
                             dt, _stream(stream))
-    _check(rc, "mxfp4_quantize")
+    if rc:
+        _check(rc, "mxfp4_quantize")
     return codes, scales
 
 
@@ -543,7 +551,8 @@ def mxfp4_dequantize(codes, scales, Y, axis: int = 1, stream=None):
     rows, K, dt = _mx_quant_args(Y, codes, scales, axis, "Y")
     rc = lib.mxfp4_dequantize(_dev(codes, "codes"), _dev(scales, "scales"), _dev(Y, "Y"), rows, K, axis,
                               dt, _stream(stream))
-    _check(rc, "mxfp4_dequantize")
+    if rc:
+        _check(rc, "mxfp4_dequantize")
     return Y
 
 
@@ -558,9 +567,13 @@ def _gemm_mx_args(A, a_scales, B, b_scales, bias, C):
         raise ValueError("A must be 2-D")
     if (K + 127) >> 7 != g or C.shape != (M, N):
         raise ValueError(f"shape mismatch: A{tuple(A.shape)} B{tuple(B.shape)} C{tuple(C.shape)}")
-    if bias is not None and bias.numel() != N:
+    if bias is None:
+        tb = None
+    elif bias.numel() == N:
+        tb = _tname(bias)
+    else:
         raise ValueError(f"bias must have N = {N} elements")
-    return M, N, K, dtypes_code(ta, "mxfp4", _tname(bias) if bias is not None else None, _tname(C))
+    return M, N, K, dtypes_code(ta, "mxfp4", tb, _tname(C))
 
 
 def gemm_mxfp4_bias_act(A, a_scales, B, b_scales, bias, C, act="none", alpha: float = 0.0, stream=None):
@@ -570,7 +583,8 @@ def gemm_mxfp4_bias_act(A, a_scales, B, b_scales, bias, C, act="none", alpha: fl
     rc = lib.gemm_mxfp4_bias_act(_dev(A, "A"), _dev(a_scales, "a_scales"), _dev(B, "B"),
                                  _dev(b_scales, "b_scales"), _dev(bias, "bias"), _dev(C, "C"), M, N, K, dt,
                                  _act(act), float(alpha), _stream(stream))
-    _check(rc, "gemm_mxfp4_bias_act")
+    if rc:
+        _check(rc, "gemm_mxfp4_bias_act")
     return C
 
 
@@ -581,7 +595,8 @@ def gemm_mxfp4_bias_add_act(A, a_scales, B, b_scales, bias, R, C, act="none", al
     rc = lib.gemm_mxfp4_bias_add_act(_dev(A, "A"), _dev(a_scales, "a_scales"), _dev(B, "B"),
                                      _dev(b_scales, "b_scales"), _dev(bias, "bias"), _residual(R, C),
                                      _dev(C, "C"), M, N, K, dt, _act(act), float(alpha), _stream(stream))
-    _check(rc, "gemm_mxfp4_bias_add_act")
+    if rc:
+        _check(rc, "gemm_mxfp4_bias_add_act")
     return C
 
 

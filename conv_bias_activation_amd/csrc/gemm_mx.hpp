@@ -104,10 +104,12 @@ __device__ __forceinline__ u32x4 shift_x8(u32x4 v, uint32_t d) {
   return all ? u32x4{0u, 0u, 0u, 0u} : v;
 }
 
-// The activation for an output of type DTO (fp32 GELU keeps its subnormal tail).
+// The activation for an output of type DTO: GELU to the accuracy that a 16-bit
+// output keeps, and with its subnormal tail for fp32.
 template <int ACT, int DTO>
 __device__ __forceinline__ float act(float z, float alpha) {
   if constexpr (ACT == ACT_GELU && DTO == DT_F32) return gelu_f32_tail(z);
+  else if constexpr (ACT == ACT_GELU) return gelu_f32_short(z);
   else return act_fn<ACT, DTO>(z, alpha);
 }
 

@@ -21,7 +21,7 @@ inline void launch_gemm_mx_to(const MxGemmArgs& a, hipStream_t s) {
   if (a.K < (DTA == DT_MXFP4 ? 1u : 8u)) return launch_mx_short<DTA, DTO>(a, s);
   if constexpr (DTA == DT_MXFP4) {
     const uint64_t tiles = (uint64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
-    if (tiles >= 128) return launch_mx_tile<DTO>(a, s);
+    if (tiles >= 64) return launch_mx_tile<DTO, 4, 2>(a, s);
   }
   if (a.M <= 16) launch_mx_stream_nb<DTA, DTO, 1>(a, s);
   else if (a.M <= 32) launch_mx_stream_nb<DTA, DTO, 2>(a, s);
