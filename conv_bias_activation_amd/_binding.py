@@ -124,6 +124,30 @@ def _load():
 lib = _load()
 
 
+def _load_native():
+    """The C++ way from torch tensors to the MXFP4 calls (native_call.cpp), or
+    None where torch or the module is missing: the calls below then marshal
+    through ctypes."""
+    import importlib.machinery
+    import importlib.util
+    path = os.path.join(_HERE, "_native.so")
+    try:
+        import torch  # noqa: F401  (its libraries have to be there first)
+    except ImportError:
+        return None
+    if not os.path.exists(path):
+        return None
+    loader = importlib.machinery.ExtensionFileLoader(__package__ + "._native", path)
+    m = importlib.util.module_from_spec(importlib.util.spec_from_loader(loader.name, loader))
+    loader.exec_module(m)
+    m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.mxfp4_quantize, lib.mxfp4_dequantize, lib.gemm_mxfp4_bias_act, lib.gemm_mxfp4_bias_add_act)))
+    return m
+
+
+_native = _load_native()
+
+
 def status_string(status: int) -> str:
     return lib.biasact_status_string(int(status)).decode()
 
@@ -537,6 +561,8 @@ def mxfp4_quantize(X, codes, scales, axis: int = 1, stream=None):
     """Quantises X to MXFP4 with blocks of 32 along `axis`: the rows of
     X[rows, K] (axis 1) or the columns of X[K, rows] (axis 0).  codes and
     scales (uint8, mxfp4_shapes(rows, K)) are written and returned."""
+    if stream is None and _native is not None and _native.quantize(X, codes, scales, axis):
+        return codes, scales
     rows, K, dt = _mx_quant_args(X, codes, scales, axis, "X")
     rc = lib.mxfp4_quantize(_dev(X, "X"), _dev(codes, "codes"), _dev(scales, "scales"), rows, K, axis,
                             dt, _stream(stream))
@@ -548,6 +574,8 @@ def mxfp4_quantize(X, codes, scales, axis: int = 1, stream=None):
 def mxfp4_dequantize(codes, scales, Y, axis: int = 1, stream=None):
     """The values that codes and scales stand for, in Y's type and in Y's
     layout ([rows, K] with axis 1, [K, rows] with axis 0)."""
+    if stream is None and _native is not None and _native.dequantize(Y, codes, scales, axis):
+        return Y
     rows, K, dt = _mx_quant_args(Y, codes, scales, axis, "Y")
     rc = lib.mxfp4_dequantize(_dev(codes, "codes"), _dev(scales, "scales"), _dev(Y, "Y"), rows, K, axis,
                               dt, _stream(stream))
@@ -579,6 +607,9 @@ def _gemm_mx_args(A, a_scales, B, b_scales, bias, C):
 def gemm_mxfp4_bias_act(A, a_scales, B, b_scales, bias, C, act="none", alpha: float = 0.0, stream=None):
     """C = act(A @ B.T + bias), B in MXFP4 (codes and b_scales of its N rows);
     A in MXFP4 (codes and a_scales), or fp16 / bf16 with a_scales None."""
+    if (stream is None and _native is not None
+            and _native.gemm(A, a_scales, B, b_scales, bias, None, C, act, alpha)):
+        return C
     M, N, K, dt = _gemm_mx_args(A, a_scales, B, b_scales, bias, C)
     rc = lib.gemm_mxfp4_bias_act(_dev(A, "A"), _dev(a_scales, "a_scales"), _dev(B, "B"),
                                  _dev(b_scales, "b_scales"), _dev(bias, "bias"), _dev(C, "C"), M, N, K, dt,
@@ -591,6 +622,9 @@ def gemm_mxfp4_bias_act(A, a_scales, B, b_scales, bias, C, act="none", alpha: fl
 def gemm_mxfp4_bias_add_act(A, a_scales, B, b_scales, bias, R, C, act="none", alpha: float = 0.0,
                             stream=None):
     """C = act(A @ B.T + bias + R); R like C (may be C itself)."""
+    if (stream is None and _native is not None and R is not None
+            and _native.gemm(A, a_scales, B, b_scales, bias, R, C, act, alpha)):
+        return C
     M, N, K, dt = _gemm_mx_args(A, a_scales, B, b_scales, bias, C)
     rc = lib.gemm_mxfp4_bias_add_act(_dev(A, "A"), _dev(a_scales, "a_scales"), _dev(B, "B"),
                                      _dev(b_scales, "b_scales"), _dev(bias, "bias"), _residual(R, C),

@@ -23,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libbiasact.so")
+NATIVE = os.path.join(PKG, "_native.so")     # torch tensors -> libbiasact.so in C++ (see native_call.cpp)
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -50,6 +51,25 @@ def _run(cmd):
     return time.time() - t0, warn
 
 
+def native_command(out: str):
+    """The compiler call for the torch side, or None without torch (the C ABI
+    and the ctypes binding do without it)."""
+    try:
+        import torch
+        from torch.utils import cpp_extension
+    except ImportError:
+        return None
+    import sysconfig
+    inc = [f"-I{p}" for p in (*cpp_extension.include_paths(), sysconfig.get_paths()["include"],
+                              os.path.join(os.path.dirname(os.path.dirname(HIPCC)), "include"), INCLUDE)]
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    # torch is loaded before this module, so its libraries need no search path
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Wno-sign-compare",
+            "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", f"-D_GLIBCXX_USE_CXX11_ABI={abi}", *inc,
+            os.path.join(CSRC, "native_call.cpp"), "-o", out, f"-L{libs}", "-ltorch_python", "-lc10", "-lc10_hip"]
+
+
 def build(jobs: int | None = None, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     jobs = jobs or min(8, os.cpu_count() or 4)
@@ -61,6 +81,9 @@ def build(jobs: int | None = None, verbose: bool = False) -> str:
         obj = os.path.join(BUILD, src + ".o")
         steps.append((src, ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-I", INCLUDE, "-I", CSRC,
                             "-c", os.path.join(CSRC, src), "-o", obj], obj))
+    native = native_command(NATIVE + ".tmp")
+    if native:
+        steps.append(("native_call.cpp", native, None))
     objs = []
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
         futs = {ex.submit(_run, cmd): (name, obj) for name, cmd, obj in steps}
@@ -71,7 +94,10 @@ def build(jobs: int | None = None, verbose: bool = False) -> str:
                 print(f"  compiled {name} in {dt:.1f}s", flush=True)
             if warn and verbose:
                 print(warn, flush=True)
-            objs.append(obj)
+            if obj:
+                objs.append(obj)
+    if native:
+        os.replace(NATIVE + ".tmp", NATIVE)
     tmp = LIB + ".tmp"
     _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *sorted(objs)])
     os.replace(tmp, LIB)

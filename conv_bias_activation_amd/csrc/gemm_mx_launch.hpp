@@ -6,13 +6,22 @@
 
 namespace biasact {
 
+inline uint64_t tiles_of(const MxGemmArgs& a, uint32_t bm, uint32_t bn) {
+  return (uint64_t)((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn);
+}
+
+// Streaming kernel of 16 MB rows of A.  Its workgroups take the 256 CUs in
+// rounds, and a round's time goes with the rows that a workgroup loads per
+// group of k: NB blocks of codes, MB blocks of A (four times the bytes when A is
+// 16-bit), and about two blocks' worth for what does not depend on them.
 template <int DTA, int DTO, int MB>
 inline void launch_mx_stream_nb(const MxGemmArgs& a, hipStream_t s) {
-  // the widest block of B that still gives every CU a workgroup
-  const uint64_t tm = (a.M + 16 * MB - 1) / (16 * MB);
-  auto tiles = [&](uint32_t nb) { return tm * ((a.N + 16 * nb - 1) / (16 * nb)); };
-  if (tiles(4) >= 256) launch_mx_stream<DTA, DTO, 4, MB, 8>(a, s);
-  else if (tiles(2) >= 256) launch_mx_stream<DTA, DTO, 2, MB, 8>(a, s);
+  auto cost = [&](uint32_t nb) {
+    return (tiles_of(a, 16 * MB, 16 * nb) + 255) / 256 * (nb + (DTA == DT_MXFP4 ? 1 : 4) * MB + 2);
+  };
+  const uint64_t c1 = cost(1), c2 = cost(2), c4 = cost(4);
+  if (c4 <= c2 && c4 <= c1) launch_mx_stream<DTA, DTO, 4, MB, 8>(a, s);
+  else if (c2 <= c1) launch_mx_stream<DTA, DTO, 2, MB, 8>(a, s);
   else launch_mx_stream<DTA, DTO, 1, MB, 8>(a, s);
 }
 
@@ -20,8 +29,18 @@ template <int DTA, int DTO>
 inline void launch_gemm_mx_to(const MxGemmArgs& a, hipStream_t s) {
   if (a.K < (DTA == DT_MXFP4 ? 1u : 8u)) return launch_mx_short<DTA, DTO>(a, s);
   if constexpr (DTA == DT_MXFP4) {
-    const uint64_t tiles = (uint64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
-    if (tiles >= 64) return launch_mx_tile<DTO, 4, 2>(a, s);
+    // Past one round of 64x64 blocks the tiled kernels are faster; between them
+    // the rounds decide.  Measured at K = 4096 (us a round): 256 workgroups of
+    // 64x64 streaming 8.3, up to 256 of 128x128 14, 512 of them 26, 256 of
+    // 256x256 40.  E.g. 512x4096: 17.0 streaming, 13.5 with 128x128; 64x16384:
+    // 10.4 and 16.1; 6464x790x7221: 44.7 with 128x128, 57.9 with 256x256; 4096^3: 52
+    // and 41.
+    if (tiles_of(a, 64, 64) > 256) {
+      const uint64_t t128 = tiles_of(a, 128, 128);
+      const uint64_t small = t128 <= 256 ? 14 : (t128 + 511) / 512 * 26, large = (tiles_of(a, 256, 256) + 255) / 256 * 40;
+      if (large < small) return launch_mx_tile<DTO, 2, 4, 4, 2>(a, s);
+      return launch_mx_tile<DTO, 2, 2, 2, 2>(a, s);
+    }
   }
   if (a.M <= 16) launch_mx_stream_nb<DTA, DTO, 1>(a, s);
   else if (a.M <= 32) launch_mx_stream_nb<DTA, DTO, 2>(a, s);

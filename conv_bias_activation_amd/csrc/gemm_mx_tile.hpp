@@ -1,26 +1,27 @@
 // gemm_mx_tile.hpp — tiled fused product of two MXFP4 operands on gfx950:
 //   C[M,N] = act(A . B^T + bias (+ R)), both operands as rows of k (mx_args.hpp)
 //
-// Workgroup: 4 waves, 2 (m) x 2 (n), of SJ x SI accumulator blocks of 32x32
-// each: an output tile of 64 SJ (m) x 64 SI (n).  A k-tile is one group of 128
-// values, 64 bytes of codes and 4 scale bytes a row.  Two workgroups share a
-// CU: one's loads, LDS reads, start and end run under the other's matrix
-// instructions, v_mfma_scale_f32_32x32x64.
+// Workgroup: WM x WN waves (m x n) of SJ x SI accumulator blocks of 32x32
+// each: an output tile of 32 SJ WM (m) x 32 SI WN (n).  A k-step is two groups of
+// 128 values, 128 bytes of codes and 8 scale bytes a row: a whole cache line
+// per row.  (With one group a step, 64 bytes a row, a CU reads at half the rate:
+// 68 against 133 GB/s measured from L2.)
 //
-// Codes reach LDS without passing through registers, 16 bytes a lane, three
-// stages deep; chunk c of row r lies at slot c ^ ((r >> 2) & 3), so the eight
-// lanes that a 16-byte LDS read serves at a time are on different banks.  Half
-// h of a wave takes chunks 2 h and 2 h + 1 of its rows: its two scale bytes
-// are then neighbours, and one shift puts them where the instruction's operand
-// selector reads byte 0 for the first k-step and byte 1 for the second.
-// Scales travel 16 bytes a row for four k-tiles at once, through registers:
-// fetched with each k-tile they would touch one cache line per row and tile,
-// as many as the codes do.
+// Codes reach LDS without passing through registers, 16 bytes a lane, two
+// stages deep; chunk c of row r lies at slot c ^ (r & 7), so the eight lanes
+// that a 16-byte LDS read serves at a time are on different banks.  The four
+// v_mfma_scale_f32_32x32x64 of a step take chunk ks of the step's first group in
+// the lower half of a wave and chunk ks of its second group in the upper half:
+// each lane then needs one scale word per row and step, whose byte ks the
+// instruction's operand selector picks.  Scales travel 16 bytes a row for two
+// steps at once, through registers: fetched with each step they would touch
+// one cache line per row, as many as the codes do.
 //
-// Epilogue: the fp32 sums leave through LDS, 32 SJ rows at a time (16-byte
-// chunk c of row r at slot c ^ 2 (r & 15)), so every lane handles eight
-// consecutive outputs of a row: one bias fetch for all its rows, whole 16-byte
-// residual loads and stores.
+// Epilogue: each lane adds the bias, applies the activation to its own sums and puts the rounded values into LDS (16-byte chunk c of row r at
+// slot c ^ r, within the row), from where whole rows are stored, 16 bytes a lane.
+// A residual comes in the same way: whole rows into LDS, then each value to the
+// lane that holds its sum.  16-bit outputs take one pass, 32-bit ones a pass for
+// each wm.
 #pragma once
 
 #include "epilogue.hpp"
@@ -29,27 +30,26 @@
 namespace biasact {
 
 namespace mxt {
-constexpr int THREADS = 256, STAGES = 3;
-
-template <int SJ, int SI>
+template <int WM, int WN, int SJ, int SI>
 struct Tile {
-  static constexpr int BM = 64 * SJ, BN = 64 * SI;
-  static constexpr int A_STAGE = BM * 64, B_STAGE = BN * 64;
-  static constexpr int A_OFF = 0, B_OFF = STAGES * A_STAGE, S_OFF = B_OFF + STAGES * B_STAGE;
-  static constexpr int LDS_BYTES = S_OFF + (BM + BN) * 16;       // 78 KB for 256x128: two workgroups a CU
-  static constexpr int SLOADS = (BM + BN + THREADS - 1) / THREADS;   // scale rows per thread
-  static constexpr int PASS_ROWS = 32 * SJ;
-  static_assert(PASS_ROWS * BN * 4 <= LDS_BYTES, "epilogue staging");
+  static constexpr int THREADS = 64 * WM * WN, BM = 32 * SJ * WM, BN = 32 * SI * WN;
+  static constexpr int A_STAGE = BM * 128, B_STAGE = BN * 128, S_BUF = (BM + BN) * 16;
+  static constexpr int A_OFF = 0, B_OFF = 2 * A_STAGE, S_OFF = B_OFF + 2 * B_STAGE;
+  static constexpr int BIAS_OFF = S_OFF + 2 * S_BUF, LDS_BYTES = BIAS_OFF + BN * 4;
+  static_assert(BN <= THREADS, "bias");
+  static constexpr int A_LOADS = BM * 128 / 16 / THREADS, B_LOADS = BN * 128 / 16 / THREADS;   // per wave and step
+  static constexpr int S_LOADS = (BM + BN) / THREADS;                                          // scale rows per thread
+  static_assert((BM + BN) % THREADS == 0, "scale rows");
+  static_assert(BM * BN * 2 <= BIAS_OFF && 32 * SJ * BN * 4 <= BIAS_OFF, "epilogue staging");
+  static_assert(LDS_BYTES <= 160 * 1024, "LDS");
 };
 
 constexpr int WAIT_LGKM0 = 0xC07F;
 constexpr int wait_vm(int n) { return 0x0F70 | (n & 0xF) | ((n >> 4) << 14); }
 
-__device__ __forceinline__ int swz(int row) { return (row >> 2) & 3; }
-
-// 16 bytes per lane from off + soff of the buffer to lds + 16 * lane
-__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t off, int soff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, off, soff, 0, 0);
+// 16 bytes per lane from off of the buffer to lds + 16 * lane
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, off, 0, 0, 0);
 }
 
 // acc += b . a^T over 64 k, scale byte KS of each word
@@ -61,9 +61,9 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 b, u32x4 a, f32x16 acc, uint32_t 
 }
 }  // namespace mxt
 
-template <int DTO, int SJ, int SI>
-__global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxGemmArgs a) {
-  using T = mxt::Tile<SJ, SI>;
+template <int DTO, int WM, int WN, int SJ, int SI>
+__global__ __launch_bounds__(64 * WM * WN, 2) void mx_tile_kernel(MxGemmArgs a) {
+  using T = mxt::Tile<WM, WN, SJ, SI>;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[T::LDS_BYTES];
 
   uint32_t tm, tn;
@@ -71,10 +71,11 @@ __global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxGemmArgs a) {
   const uint32_t m0 = tm * T::BM, n0 = tn * T::BN;
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = w >> 1, wn = w & 1;
+  const int wm = w / WN, wn = w % WN;
   const int half = lane >> 5, lrow = lane & 31;
   const int G = (int)a.G;                     // >= 1
 
+  // sums of n = 32 si + 8 (e / 4) + 4 half + e % 4, m = 32 sj + lrow of the wave's block
   f32x16 acc[SI][SJ];
 #pragma unroll
   for (int si = 0; si < SI; ++si)
@@ -83,221 +84,274 @@ __global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxGemmArgs a) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[si][sj][r] = 0.0f;
 
-  // ---- direct loads: SJ of A and SI of B per wave and k-tile, 16 rows each --------
-  const __amdgpu_buffer_rsrc_t ra = make_rsrc(a.A, a.a_bytes);
-  const __amdgpu_buffer_rsrc_t rb = make_rsrc(a.B, a.b_bytes);
-  uint32_t a_off[SJ], b_off[SI];              // rows past the end read as zero
+  // ---- direct loads: 8 rows of 128 bytes each ---------------------------------------
+  // Rows past the end read as zeros (or, where a huge offset wraps, as other
+  // rows); their sums are not stored.  The main loop has no branches: loads for
+  // which there is no step have a buffer of no bytes, i.e. fetch nothing.
+  const uint32_t chunk = (lane & 7) ^ (lane >> 3);     // that goes to slot lane % 8 of row lane / 8
+  const uint32_t a_off = (m0 + T::A_LOADS * 8 * w + (lane >> 3)) * a.G * 64u + chunk * 16u;
+  const uint32_t b_off = (n0 + T::B_LOADS * 8 * w + (lane >> 3)) * a.G * 64u + chunk * 16u;
+  constexpr int LOADS = T::A_LOADS + T::B_LOADS;
+  // loads [from, to) of this wave's share of step s, into stage st
+  auto issue = [&](int s, int st, int from, int to) {
+    const bool more = 2 * s < G;
+    const __amdgpu_buffer_rsrc_t ra = make_rsrc(a.A, more ? a.a_bytes : 0u);
+    const __amdgpu_buffer_rsrc_t rb = make_rsrc(a.B, more ? a.b_bytes : 0u);
+    // with an odd G the last step's second group reads as zero
+    const bool cut = 2 * s + 1 >= G && chunk >= 4u;
 #pragma unroll
-  for (int i = 0; i < SJ; ++i) {
-    const int row = (SJ * w + i) * 16 + (lane >> 2);
-    a_off[i] = m0 + row < a.M ? (m0 + row) * a.G * 64u + ((lane & 3) ^ mxt::swz(row)) * 16u : kOOB;
-  }
-#pragma unroll
-  for (int i = 0; i < SI; ++i) {
-    const int row = (SI * w + i) * 16 + (lane >> 2);
-    b_off[i] = n0 + row < a.N ? (n0 + row) * a.G * 64u + ((lane & 3) ^ mxt::swz(row)) * 16u : kOOB;
-  }
-  auto issue = [&](int kt, int st) {
-#pragma unroll
-    for (int i = 0; i < SJ; ++i)
-      mxt::load_to_lds(ra, smem + T::A_OFF + st * T::A_STAGE + (SJ * w + i) * 1024, a_off[i], kt * 64);
-#pragma unroll
-    for (int i = 0; i < SI; ++i)
-      mxt::load_to_lds(rb, smem + T::B_OFF + st * T::B_STAGE + (SI * w + i) * 1024, b_off[i], kt * 64);
+    for (int i = 0; i < LOADS; ++i) {
+      if (i < from || i >= to) continue;
+      if (i < T::A_LOADS)
+        mxt::load_to_lds(ra, smem + T::A_OFF + st * T::A_STAGE + (T::A_LOADS * w + i) * 1024,
+                         cut ? kOOB : a_off + (8u * i * a.G * 64u + s * 128u));
+      else
+        mxt::load_to_lds(rb, smem + T::B_OFF + st * T::B_STAGE + (T::B_LOADS * w + i - T::A_LOADS) * 1024,
+                         cut ? kOOB : b_off + (8u * (i - T::A_LOADS) * a.G * 64u + s * 128u));
+    }
   };
 
-  // ---- scales: thread t brings rows t (and t + 256) of A's rows followed by B's -----
-  // words 4 S .. 4 S + 3 of the row, zero from G on (never past the row's own)
-  auto load_scales = [&](int S, u32x4 (&v)[T::SLOADS]) {
+  // ---- scales: thread t brings rows t (and t + THREADS) of A's rows followed by B's ---
+  // Words 4 S .. 4 S + 3 of the row, zero from G on.  first: S == 0 and any G, a
+  // load never goes past the row's own words.  Else G > 4, and a load that would
+  // brings the row's last four, shifted down by put_scales.
+  auto load_scales = [&](int S, bool first, u32x4 (&v)[T::S_LOADS]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < T::SLOADS; ++i) {
-      const int row0 = i * mxt::THREADS + 64 * w;      // uniform; BM and BN are multiples of 64
-      const bool of_a = row0 < T::BM;
-      const __amdgpu_buffer_rsrc_t rs = of_a ? make_rsrc(a.As, a.as_bytes) : make_rsrc(a.Bs, a.bs_bytes);
+    for (int i = 0; i < T::S_LOADS; ++i) {
+      const int row0 = i * T::THREADS + 64 * w;        // uniform; BM and BN are multiples of 64
+      const bool of_a = row0 < T::BM, any = first || 4 * S < G;
+      const __amdgpu_buffer_rsrc_t rs =
+          of_a ? make_rsrc(a.As, any ? a.as_bytes : 0u) : make_rsrc(a.Bs, any ? a.bs_bytes : 0u);
       const uint32_t row = of_a ? m0 + row0 + lane : n0 + (row0 - T::BM) + lane;
-      const bool ok = row0 < T::BM + T::BN && row < (of_a ? a.M : a.N);
-      const uint32_t at = (row * a.G + 4u * S) * 4u;
-      v[i] = u32x4{0, 0, 0, 0};
-      if (4 * S + 4 <= G) {
-        v[i] = ld_b128(rs, ok ? at : kOOB);
+      if (!first) {
+        v[i] = ld_b128(rs, (row * a.G + min(4 * S, G - 4)) * 4u);
+      } else if (G >= 4) {
+        v[i] = ld_b128(rs, row * a.G * 4u);
       } else {
+        v[i] = u32x4{0, 0, 0, 0};
 #pragma unroll
         for (int e = 0; e < 3; ++e)
-          if (4 * S + e < G) v[i][e] = ld_b32(rs, ok ? at + e * 4u : kOOB);
+          if (e < G) v[i][e] = ld_b32(rs, (row * a.G + e) * 4u);
       }
     }
   };
-  auto put_scales = [&](const u32x4 (&v)[T::SLOADS]) {
+  auto put_scales = [&](int S, const u32x4 (&v)[T::S_LOADS]) __attribute__((always_inline)) {
+    const int d = S == 0 ? 0 : 4 * S - min(4 * S, G - 4);
+    const bool one = d & 1, two = d & 2;               // uniform
 #pragma unroll
-    for (int i = 0; i < T::SLOADS; ++i)
-      if (i * mxt::THREADS + 64 * w < T::BM + T::BN)
-        *reinterpret_cast<u32x4*>(smem + T::S_OFF + (i * mxt::THREADS + 64 * w + lane) * 16) = v[i];
+    for (int i = 0; i < T::S_LOADS; ++i) {
+      u32x4 o = v[i];
+      o = one ? u32x4{o.y, o.z, o.w, 0u} : o;
+      o = two ? u32x4{o.z, o.w, 0u, 0u} : o;
+      *reinterpret_cast<u32x4*>(smem + T::S_OFF + (S & 1) * T::S_BUF + (i * T::THREADS + 64 * w + lane) * 16) = o;
+    }
   };
 
-  // ---- LDS fragment addresses: row, chunk 2 half + ks ------------------------------
-  const int x = mxt::swz(lrow);
-  uint32_t a_rd[2], b_rd[2];
-#pragma unroll
-  for (int ks = 0; ks < 2; ++ks) {
-    a_rd[ks] = T::A_OFF + (wm * 32 * SJ + lrow) * 64 + (((2 * half + ks) ^ x) * 16);
-    b_rd[ks] = T::B_OFF + (wn * 32 * SI + lrow) * 64 + (((2 * half + ks) ^ x) * 16);
-  }
+  // ---- LDS fragment addresses: row, chunk 4 half + ks ------------------------------
+  const uint32_t fr = lrow * 128 + (((4 * half) ^ (lrow & 7)) * 16);
+  const uint32_t a_rd = T::A_OFF + wm * 32 * SJ * 128 + fr, b_rd = T::B_OFF + wn * 32 * SI * 128 + fr;
 
   // ---- main loop ---------------------------------------------------------------------
-  // k-tile kt: wait for this wave's loads of it (those of kt + 1 may be in
-  // flight), barrier, issue kt + 2 into the stage that kt - 1 held (every wave
-  // had its fragments before it came to this barrier), read fragments, multiply.
-  constexpr int LOADS = SJ + SI;
-  u32x4 snext[T::SLOADS];
-  load_scales(0, snext);
-  issue(0, 0);
-  if (G > 1) issue(1, 1);
-  put_scales(snext);
-  u32x4 sa[SJ], sb[SI];
-  const int sh = 16 * half;
-  int st = 0;                                          // kt % 3
-  for (int k0 = 0; k0 < G; k0 += 4) {
+  // Step s: this wave's loads of it have landed; barrier; issue step s + 1 into
+  // the stage that s - 1 held (every wave had its fragments of s - 1 before it
+  // came to this barrier); read fragments and multiply.  Scale words of the
+  // next two steps are loaded in even steps and put in odd ones, into the
+  // buffer whose last readers came to the barrier before.
+  const int steps = (G + 1) >> 1;
+  u32x4 snext[T::S_LOADS];
+  // this tile's bias (zeros past N or without one): its bits now, fp32 into LDS later
+  const __amdgpu_buffer_rsrc_t rbias = make_rsrc(a.bias, a.bias_dt >= 0 ? a.bias_bytes : 0u);
+  const uint32_t bias_n = n0 + threadIdx.x;
+  const bool bias_ok = threadIdx.x < T::BN && bias_n < a.N;
+  uint32_t bias;
+  if (a.bias_dt == DT_F32) bias = ld_b32(rbias, bias_ok ? bias_n * 4u : kOOB);
+  else bias = ld_b16(rbias, bias_ok ? bias_n * 2u : kOOB);
+  load_scales(0, true, snext);
+  issue(0, 0, 0, LOADS);
+  put_scales(0, snext);
+  if (threadIdx.x < T::BN)
+    *reinterpret_cast<float*>(smem + T::BIAS_OFF + threadIdx.x * 4) =
+        a.bias_dt == DT_F16 ? widen<DT_F16>(bias) : a.bias_dt == DT_BF16 ? widen<DT_BF16>(bias) : widen<DT_F32>(bias);
+  auto step = [&](int s, int odd) __attribute__((always_inline)) {
+    __builtin_amdgcn_s_waitcnt(mxt::wait_vm(0));
+    __builtin_amdgcn_s_waitcnt(mxt::WAIT_LGKM0);       // the scales this wave put
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    const int S = s >> 1;
+    const uint8_t* sp = smem + T::S_OFF + (S & 1) * T::S_BUF + (2 * odd + half) * 4;
+    uint32_t wa[SJ], wb[SI];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int kt = k0 + j;
-      if (kt >= G) break;
-      if (kt + 1 < G) __builtin_amdgcn_s_waitcnt(mxt::wait_vm(LOADS));
-      else __builtin_amdgcn_s_waitcnt(mxt::wait_vm(0));
-      __builtin_amdgcn_s_waitcnt(mxt::WAIT_LGKM0);     // the scales this wave put
+    for (int si = 0; si < SI; ++si)
+      wb[si] = *reinterpret_cast<const uint32_t*>(sp + (T::BM + wn * 32 * SI + si * 32 + lrow) * 16);
+#pragma unroll
+    for (int sj = 0; sj < SJ; ++sj)
+      wa[sj] = *reinterpret_cast<const uint32_t*>(sp + (wm * 32 * SJ + sj * 32 + lrow) * 16);
+    u32x4 fa[2][SJ], fb[2][SI];
+    uint32_t ar = a_rd, br = b_rd;
+    if constexpr (SJ * SI > 4) asm volatile("" : "+v"(ar), "+v"(br));   // no registers for each chunk's address
+    auto read = [&](int ks) {
+#pragma unroll
+      for (int si = 0; si < SI; ++si)
+        fb[ks & 1][si] = *reinterpret_cast<const u32x4*>(smem + (br ^ (16u * ks)) + odd * T::B_STAGE + si * 4096);
+#pragma unroll
+      for (int sj = 0; sj < SJ; ++sj)
+        fa[ks & 1][sj] = *reinterpret_cast<const u32x4*>(smem + (ar ^ (16u * ks)) + odd * T::A_STAGE + sj * 4096);
+    };
+    auto multiply = [&](auto ks_c) __attribute__((always_inline)) {
+      constexpr int ks = decltype(ks_c)::value;
       __builtin_amdgcn_sched_barrier(0);
-      __builtin_amdgcn_s_barrier();
-      __builtin_amdgcn_sched_barrier(0);
-      const int st2 = st == 0 ? 2 : st - 1;            // (kt + 2) % 3
-      if (kt + 2 < G) issue(kt + 2, st2);
-      if (j == 0) {
-        // every wave put its rows at least one barrier ago; the words stay in
-        // registers, and the next four k-tiles' go in from j = 2 on, when every
-        // wave has passed the barrier after these reads
-#pragma unroll
-        for (int sj = 0; sj < SJ; ++sj)
-          sa[sj] = *reinterpret_cast<const u32x4*>(smem + T::S_OFF + (wm * 32 * SJ + sj * 32 + lrow) * 16);
-#pragma unroll
-        for (int si = 0; si < SI; ++si)
-          sb[si] = *reinterpret_cast<const u32x4*>(smem + T::S_OFF + (T::BM + wn * 32 * SI + si * 32 + lrow) * 16);
-        if (k0 + 4 < G) load_scales((k0 >> 2) + 1, snext);
-      }
-      if (j == 2 && k0 + 4 < G) put_scales(snext);
-      u32x4 fa[SJ][2], fb[SI][2];
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-#pragma unroll
-        for (int si = 0; si < SI; ++si)
-          fb[si][ks] = *reinterpret_cast<const u32x4*>(smem + b_rd[ks] + st * T::B_STAGE + si * 2048);
-#pragma unroll
-        for (int sj = 0; sj < SJ; ++sj)
-          fa[sj][ks] = *reinterpret_cast<const u32x4*>(smem + a_rd[ks] + st * T::A_STAGE + sj * 2048);
-      }
 #pragma unroll
       for (int si = 0; si < SI; ++si)
 #pragma unroll
         for (int sj = 0; sj < SJ; ++sj)
-          acc[si][sj] = mxt::mfma32<0>(fb[si][0], fa[sj][0], acc[si][sj], sb[si][j] >> sh, sa[sj][j] >> sh);
-#pragma unroll
-      for (int si = 0; si < SI; ++si)
-#pragma unroll
-        for (int sj = 0; sj < SJ; ++sj)
-          acc[si][sj] = mxt::mfma32<1>(fb[si][1], fa[sj][1], acc[si][sj], sb[si][j] >> sh, sa[sj][j] >> sh);
-      st = st == 2 ? 0 : st + 1;
-    }
+          acc[si][sj] = mxt::mfma32<ks>(fb[ks & 1][si], fa[ks & 1][sj], acc[si][sj], wb[si], wa[sj]);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    // The next fragments' reads and a share of the next step's loads go out
+    // before each quarter's matrix instructions: all loads at once would hold up
+    // the reads behind them.
+    read(0);
+    if (odd == 0) load_scales(S + 1, false, snext);
+    read(1);
+    issue(s + 1, odd ^ 1, 0, (LOADS + 2) / 3);
+    multiply(std::integral_constant<int, 0>{});
+    read(2);
+    issue(s + 1, odd ^ 1, (LOADS + 2) / 3, 2 * ((LOADS + 2) / 3));
+    multiply(std::integral_constant<int, 1>{});
+    read(3);
+    issue(s + 1, odd ^ 1, 2 * ((LOADS + 2) / 3), LOADS);
+    if (odd == 1) put_scales(S + 1, snext);
+    multiply(std::integral_constant<int, 2>{});
+    multiply(std::integral_constant<int, 3>{});
+  };
+  for (int s = 0; s < steps; s += 2) {
+    step(s, 0);
+    if (s + 1 < steps) step(s + 1, 1);
   }
+  // no direct load (of zeros) may still be writing LDS when the epilogue reuses it
+  __builtin_amdgcn_s_waitcnt(mxt::wait_vm(0));
 
   // ---- epilogue -------------------------------------------------------------------
   const __amdgpu_buffer_rsrc_t rc = make_rsrc(a.C, a.c_bytes);
   const __amdgpu_buffer_rsrc_t rr = make_rsrc(a.R, a.R ? a.c_bytes : 0u);
-  constexpr uint32_t ES = Elem<DTO>::bytes;
-  constexpr int LPR = T::BN / 8;                       // lanes per row
-  // whole 16-byte accesses: rows of a multiple of 8 outputs, aligned bases
-  const bool vec = a.N % 8 == 0 && ((reinterpret_cast<uintptr_t>(a.C) | reinterpret_cast<uintptr_t>(a.R)) & 15u) == 0;
-  auto slot = [](int r, int c) { return (uint32_t)(r * (T::BN * 4) + ((c ^ (2 * (r & 15))) << 4)); };
-  // this lane's outputs of a row: eight consecutive ones, or columns lane + 64 e
-  const int lc = lane % LPR;
-  uint32_t idx[8];
-  float bv[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) idx[e] = vec ? n0 + 8 * lc + e : n0 + lane + 64 * (e % SI);
-  load_bias_vec<8>(a.bias, a.bias_bytes, a.bias_dt, idx, a.N, bv);
-#pragma unroll
-  for (int pass = 0; pass < 2; ++pass) {
-    __syncthreads();                                   // the last k-tile, or the previous pass, is read
-    if (wm == pass) {
-#pragma unroll
-      for (int si = 0; si < SI; ++si)
-#pragma unroll
-        for (int sj = 0; sj < SJ; ++sj)
-#pragma unroll
-          for (int g = 0; g < 4; ++g)
-            *reinterpret_cast<f32x4*>(smem + slot(sj * 32 + lrow, wn * 8 * SI + si * 8 + 2 * g + half)) =
-                f32x4{acc[si][sj][4 * g + 0], acc[si][sj][4 * g + 1], acc[si][sj][4 * g + 2], acc[si][sj][4 * g + 3]};
+  constexpr int ES = Elem<DTO>::bytes, EPC = 16 / ES;  // bytes an output, outputs a chunk
+  constexpr int CPR = T::BN / EPC;                     // chunks, and lanes, a row
+  constexpr int PASSES = ES == 2 ? 1 : WM, ROWS = T::BM / PASSES;
+  // whole 16-byte accesses: rows of whole chunks, aligned bases
+  const bool vec = a.N % EPC == 0 && ((reinterpret_cast<uintptr_t>(a.C) | reinterpret_cast<uintptr_t>(a.R)) & 15u) == 0;
+  // The thread's number, told to the compiler anew: addresses computed from it
+  // here would otherwise be kept in registers through the main loop.
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  auto slot = [](int r, int c) { return (uint32_t)(r * (T::BN * ES) + ((c ^ (r & (CPR - 1))) << 4)); };
+  // f(LDS address, element offset in C, whether there is such an output), for
+  // every chunk of the pass's rows, a row's chunks in neighbouring lanes
+  auto by_chunk = [&](int pass, auto&& f) __attribute__((always_inline)) {
+#pragma unroll 4
+    for (int it = 0; it < ROWS * CPR / T::THREADS; ++it) {
+      const int r = it * (T::THREADS / CPR) + tid / CPR, c = tid % CPR;
+      const uint32_t m = m0 + pass * ROWS + r, n = n0 + c * EPC;
+      f(slot(r, c), m * a.N + n, m < a.M && n < a.N);
     }
-    __syncthreads();
-    const uint32_t mp = m0 + pass * T::PASS_ROWS;
-    with_act(a.act, [&](auto act_c) __attribute__((always_inline)) {
-      constexpr int ACT = decltype(act_c)::value;
+  };
+  // the same for every single output
+  auto by_output = [&](int pass, auto&& f) __attribute__((always_inline)) {
+    for (int it = 0; it < ROWS / (WM * WN); ++it)
+#pragma unroll
+      for (int e = 0; e < T::BN / 64; ++e) {
+        const int r = it * (WM * WN) + w, c = (tid & 63) + 64 * e;
+        const uint32_t m = m0 + pass * ROWS + r, n = n0 + c;
+        f(slot(r, c / EPC) + (c % EPC) * ES, m * a.N + n, m < a.M && n < a.N);
+      }
+  };
+#pragma unroll 1
+  for (int pass = 0; pass < PASSES; ++pass) {
+    asm volatile("" : "+v"(tid));
+    const int row = tid & 31, four = 4 * ((tid >> 5) & 1);
+    __syncthreads();                                   // the last k-step, or the previous pass, is read
+    if (a.R) {
       if (vec) {
-        with_residual(a.R != nullptr, [&](auto res_c) __attribute__((always_inline)) {
-          constexpr bool HAS_R = decltype(res_c)::value;
-          constexpr int STEP = mxt::THREADS / LPR;
-#pragma unroll 2
-          for (int it = 0; it < T::PASS_ROWS / STEP; ++it) {
-            const int r = it * STEP + (int)threadIdx.x / LPR;
-            const uint32_t m = mp + r, n = n0 + lc * 8;
-            const bool ok = m < a.M && n < a.N;
-            const uint32_t at = m * a.N + n;
-            float z[8], rv[8];
-            if constexpr (HAS_R) {
-              load4<DTO>(rr, at, ok, *reinterpret_cast<float(*)[4]>(rv));
-              load4<DTO>(rr, at + 4, ok, *reinterpret_cast<float(*)[4]>(rv + 4));
-            }
-            const f32x4 lo = *reinterpret_cast<const f32x4*>(smem + slot(r, 2 * lc));
-            const f32x4 hi = *reinterpret_cast<const f32x4*>(smem + slot(r, 2 * lc + 1));
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              z[e] = (e < 4 ? lo[e & 3] : hi[e & 3]) + bv[e];
-              if constexpr (HAS_R) z[e] += rv[e];
-              z[e] = mx::act<ACT, DTO>(z[e], a.alpha);
-            }
-            if constexpr (ES == 4) {
-              store4<DTO>(rc, at, ok, z[0], z[1], z[2], z[3]);
-              store4<DTO>(rc, at + 4, ok, z[4], z[5], z[6], z[7]);
-            } else {
-              u32x4 o;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o[e] = narrow<DTO>(z[2 * e]) | (narrow<DTO>(z[2 * e + 1]) << 16);
-              st_b128(rc, ok ? at * ES : kOOB, o);
-            }
-          }
+        by_chunk(pass, [&](uint32_t p, uint32_t at, bool ok) {
+          *reinterpret_cast<u32x4*>(smem + p) = ld_b128(rr, ok ? at * ES : kOOB);
         });
       } else {
-        for (int it = 0; it < T::PASS_ROWS / 4; ++it) {
-          const int r = it * 4 + w;
-          const uint32_t m = mp + r;
-#pragma unroll
-          for (int e = 0; e < SI; ++e) {
-            const int c = lane + 64 * e;
-            const bool ok = m < a.M && n0 + c < a.N;
-            const uint32_t at = m * a.N + n0 + c;
-            float z = *reinterpret_cast<const float*>(smem + slot(r, c >> 2) + (c & 3) * 4) + bv[e];
-            if (a.R) z += load1<DTO>(rr, at, ok);
-            store1<DTO>(rc, at, ok, mx::act<ACT, DTO>(z, a.alpha));
-          }
-        }
+        by_output(pass, [&](uint32_t p, uint32_t at, bool ok) {
+          if constexpr (ES == 4) *reinterpret_cast<uint32_t*>(smem + p) = ld_b32(rr, ok ? at * ES : kOOB);
+          else *reinterpret_cast<uint16_t*>(smem + p) = ld_b16(rr, ok ? at * ES : kOOB);
+        });
       }
-    });
+      __syncthreads();
+    }
+    if (PASSES == 1 || wm == pass) {
+      with_act(a.act, [&](auto act_c) __attribute__((always_inline)) {
+        constexpr int ACT = decltype(act_c)::value;
+        with_residual(a.R != nullptr, [&](auto res_c) __attribute__((always_inline)) {
+#pragma unroll
+          for (int si = 0; si < SI; ++si)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              const int n = (wn * SI + si) * 32 + 8 * g + four;
+              const f32x4 bias = *reinterpret_cast<const f32x4*>(smem + T::BIAS_OFF + n * 4);
+#pragma unroll
+              for (int sj = 0; sj < SJ; ++sj) {
+                // four consecutive outputs; no other lane touches them.  One group at
+                // a time: there are few registers beside the sums.
+                __builtin_amdgcn_sched_barrier(0);
+                const int r = (PASSES == 1 ? wm * 32 * SJ : 0) + sj * 32 + row;
+                uint8_t* p = smem + slot(r, n / EPC) + (n % EPC) * ES;
+                float z[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z[e] = acc[si][sj][4 * g + e] + bias[e];
+                if constexpr (ES == 2) {
+                  if constexpr (decltype(res_c)::value) {
+                    const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) z[e] += widen<DTO>((v[e >> 1] >> (16 * (e & 1))) & 0xffffu);
+                  }
+                  u32x2 o;
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+                    o[e] = narrow<DTO>(mx::act<ACT, DTO>(z[2 * e], a.alpha)) |
+                           (narrow<DTO>(mx::act<ACT, DTO>(z[2 * e + 1], a.alpha)) << 16);
+                  *reinterpret_cast<u32x2*>(p) = o;
+                } else {
+                  if constexpr (decltype(res_c)::value) {
+                    const f32x4 v = *reinterpret_cast<const f32x4*>(p);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) z[e] += v[e];
+                  }
+                  f32x4 o;
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) o[e] = mx::act<ACT, DTO>(z[e], a.alpha);
+                  *reinterpret_cast<f32x4*>(p) = o;
+                }
+              }
+            }
+        });
+      });
+    }
+    __syncthreads();
+    if (vec) {
+      by_chunk(pass, [&](uint32_t p, uint32_t at, bool ok) {
+        st_b128(rc, ok ? at * ES : kOOB, *reinterpret_cast<const u32x4*>(smem + p));
+      });
+    } else {
+      by_output(pass, [&](uint32_t p, uint32_t at, bool ok) {
+        if constexpr (ES == 4) st_b32(rc, ok ? at * ES : kOOB, *reinterpret_cast<const uint32_t*>(smem + p));
+        else st_b16(rc, ok ? at * ES : kOOB, *reinterpret_cast<const uint16_t*>(smem + p));
+      });
+    }
   }
 }
 
-template <int DTO, int SJ, int SI>
+template <int DTO, int WM, int WN, int SJ, int SI>
 inline void launch_mx_tile(MxGemmArgs a, hipStream_t s) {
-  using T = mxt::Tile<SJ, SI>;
+  using T = mxt::Tile<WM, WN, SJ, SI>;
   a.tiles_n = (a.N + T::BN - 1) / T::BN;
   a.tiles_m = (a.M + T::BM - 1) / T::BM;
   note_launch("gemm mxfp4 tile, %d m x %d n", T::BM, T::BN);
-  launch_kernel(mx_tile_kernel<DTO, SJ, SI>, dim3(a.tiles_m * a.tiles_n), dim3(mxt::THREADS), s, a);
+  launch_kernel(mx_tile_kernel<DTO, WM, WN, SJ, SI>, dim3(a.tiles_m * a.tiles_n), dim3(T::THREADS), s, a);
 }
 
 }  // namespace biasact

@@ -323,6 +323,35 @@ def test_residual_in_place_and_equal_bits(ba, kind):
         assert torch.equal(C1, C2)
 
 
+def test_both_ways_of_the_binding_agree(ba):
+    # the C++ way takes these calls itself; with a stream given they go through ctypes
+    n = ba._binding._native
+    assert n is not None
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(33, 300, generator=g, device="cuda").half()
+    w = torch.randn(300, 72, generator=g, device="cuda")
+    u8 = lambda shape: torch.empty(shape, dtype=torch.uint8, device="cuda")
+    st = torch.cuda.current_stream()
+    got = []
+    for stream in (None, st, st.cuda_stream):
+        wc, ws = map(u8, ba.mxfp4_shapes(72, 300))
+        xc, xs = map(u8, ba.mxfp4_shapes(33, 300))
+        ba.mxfp4_quantize(w, wc, ws, axis=0, stream=stream)
+        ba.mxfp4_quantize(x, xc, xs, stream=stream)
+        back = ba.mxfp4_dequantize(xc, xs, torch.empty_like(x), stream=stream)
+        R = torch.ones(33, 72, device="cuda")
+        C = [torch.empty(33, 72, device="cuda") for _ in range(3)]
+        ba.gemm_mxfp4_bias_act(xc, xs, wc, ws, None, C[0], "leaky_relu", 0.25, stream=stream)
+        ba.gemm_mxfp4_bias_act(x, None, wc, ws, x[0, :72].contiguous(), C[1], "tanh", stream=stream)
+        ba.gemm_mxfp4_bias_add_act(x, None, wc, ws, None, R, C[2], stream=stream)
+        got.append([wc, ws, xc, xs, back, *C])
+    for other in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got[0], other))
+    assert n.quantize(x, got[0][2], got[0][3], 1) is True
+    assert n.gemm(x, None, wc, ws, None, R, C[2], "none", 0.0) is True
+    assert n.gemm(x, None, wc, ws, None, R.half(), C[2], "none", 0.0) is False
+
+
 # ---- streams and graphs -----------------------------------------------------------------
 
 @pytest.mark.parametrize("M,N,K", [(4, 512, 512), (256, 512, 512), (1024, 1024, 512)])

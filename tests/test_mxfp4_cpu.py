@@ -180,3 +180,24 @@ def test_binding_refuses():
         with pytest.raises(ValueError):
             f()
             pytest.fail(f"call {i} was accepted")
+
+
+# ---- the C++ way of the binding -------------------------------------------------------
+
+def test_native_call_declines_what_it_does_not_take():
+    n = ba._binding._native
+    if n is None:
+        pytest.skip("built without torch")
+    x, c, s, w, ws, y = torch.zeros(4, 200), _u8(4, 128), _u8(4, 8), _u8(6, 128), _u8(6, 8), torch.zeros(4, 6)
+    for args in ((), (x, c, s), (x, c, s, 1), (x, c, s, 1.0), (x, c, s, None), (None, c, s, 1), (x, 3, "s", 1),
+                 (x[0], c, s, 1), (x, c[0], s[0], 1), (x, c, s, 1 << 80), (object(),) * 4):
+        assert n.quantize(*args) is False and n.dequantize(*args) is False
+    good = [c, s, w, ws, None, None, y, "relu", 0.0]
+    assert n.gemm(*good) is False                          # host tensors
+    for i, bad in [(i, b) for i in range(9) for b in (None, 7, "x", x[0], torch.zeros(4, 6).int())]:
+        assert n.gemm(*good[:i], bad, *good[i + 1:]) is False
+    assert n.gemm(*good[:8]) is False and n.gemm() is False
+    with pytest.raises(TypeError):
+        n.bind(1, 2)
+    with pytest.raises(TypeError):
+        n.bind(1, 2, 3, "x")
