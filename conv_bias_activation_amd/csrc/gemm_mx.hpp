@@ -7,15 +7,16 @@
 // sums through LDS at the end, in wave order, so every result has one fixed
 // order of additions.
 //
-// k advances by groups of 128.  Four neighbouring lanes load 64 consecutive
-// bytes of one row: a load then touches 16 cache lines, where the layout of
-// the matrix instructions (lanes r, r + 16, r + 32, r + 48 share row r) would
-// touch 64, and the address unit takes one a cycle.  Each wave turns that into
-// the instruction's layout through LDS of its own, a row's 16-byte chunk c at
-// slot c ^ ((row >> 2) & 3) so that neither side meets a bank twice; a wave's
-// LDS operations run in order, so this needs no barrier.  A register is loaded
-// anew, for the group that is UN further, as soon as it has gone to LDS.  Scale
-// words come for four groups at a time, one row a lane.
+// k advances by units of two groups of 128.  Eight neighbouring lanes load 128
+// consecutive bytes, a cache line, of one row: a load then touches 8 lines,
+// where the layout of the matrix instructions (lanes r, r + 16, r + 32, r + 48
+// share row r) would touch 64, and a CU reads from L2 at 133 GB/s instead of 68
+// with half lines and 30 with quarters of them.  Each wave turns that into the
+// instruction's layout through LDS of its own, a row's 16-byte chunk c at slot
+// c ^ (row & 7) so that neither side meets a bank twice; a wave's LDS operations
+// run in order, so this needs no barrier.  A register is loaded anew, for the
+// unit that is UN further, as soon as it has gone to LDS.  Scale words come for
+// two units at a time, one row a lane.
 //   MXFP4 A: v_mfma_scale_f32_16x16x128, lane (r, g) with block g of row r and
 //     its scale (byte g of the word, shifted down).
 //   16-bit A: v_mfma_f32_16x16x32 c covers block c, lane (r, g) the eight k from
@@ -87,13 +88,6 @@ __device__ __forceinline__ float scale_value(uint32_t b) {
 // order; this keeps the compiler from exchanging them).
 __device__ __forceinline__ void lds_order() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
-// Eight 16-bit values; p need only be aligned for one.
-__device__ __forceinline__ u32x4 load_x8(const uint8_t* p) {
-  u32x4 v;
-  __builtin_memcpy(&v, p, 16);
-  return v;
-}
-
 // Eight values shifted down by d of them, zeros from above; d >= 8: all zero.
 __device__ __forceinline__ u32x4 shift_x8(u32x4 v, uint32_t d) {
   const bool odd = d & 1u, two = d & 2u, four = d & 4u, all = d >= 8u;
@@ -115,18 +109,19 @@ __device__ __forceinline__ float act(float z, float alpha) {
 
 }  // namespace mx
 
-// NB, MB: blocks of 16 rows of B and A per wave; NW: waves along k; UN: groups
-// of 128 k that a wave has under way.
-template <int DTA, int DTO, int NB, int MB, int NW, int UN>
+// NB, MB: blocks of 16 rows of B and A per wave; NW: waves along k; UN: units of
+// 256 k that a wave has under way; XS: pieces of 64 k of a 16-bit A (4 UN, or 2).
+template <int DTA, int DTO, int NB, int MB, int NW, int UN, int XS>
 __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxGemmArgs a) {
   constexpr int TN = 16 * NB, TM = 16 * MB;
-  // Per wave: one group of B, one piece of A (1 KB per 16 rows), four groups'
-  // scale words; at the end the waves' sums, [m][n] with n contiguous and 4
-  // floats of padding a row, which keeps the rows of one access on different
-  // banks.
+  constexpr bool LATE = NB * MB == 16;                 // the widest block: every register counts
+  // Per wave: one unit of B, one piece (MXFP4: unit) of A, 2 KB per 16 rows, and
+  // two units' scale words; at the end the waves' sums, [m][n] with n contiguous
+  // and 4 floats of padding a row, which keeps the rows of one access on
+  // different banks.
   constexpr int LDR = TN + 4;
   constexpr int SROWS = TN + (DTA == DT_MXFP4 ? TM : 0);
-  constexpr int W_AT = 0, X_AT = NB * 1024, S_AT = X_AT + MB * 1024, WAVE = S_AT + SROWS * 16;
+  constexpr int W_AT = 0, X_AT = NB * 2048, S_AT = X_AT + MB * 2048, WAVE = S_AT + SROWS * 16;
   constexpr int SUMS = TM * LDR * 4;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[NW * (WAVE > SUMS ? WAVE : SUMS)];
 
@@ -137,45 +132,45 @@ __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxGemmArgs a) {
   const uint32_t lane = threadIdx.x & 63;
   const uint32_t w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t r = lane & 15, g = lane >> 4;        // the matrix instructions' lane layout
-  const uint32_t lr = lane >> 2, lc = lane & 3;       // the loads': row, 16-byte chunk
+  const uint32_t lr = lane >> 3, lc = lane & 7;       // the loads': row (and row + 8), 16-byte chunk
   uint8_t* const my = smem + w * WAVE;
-  const uint32_t put = lr * 64u + ((lc ^ (lr >> 2)) << 4);            // a loaded chunk's place
-  const uint32_t get = r * 64u, sw = r >> 2;                          // row r's chunk c: get + ((c ^ sw) << 4)
+  const uint32_t put = lr * 128u + ((lc ^ lr) << 4);  // a loaded chunk's place; row + 8: 1024 further
+  const uint32_t get = r * 128u, sw = r & 7;          // row r's chunk c: get + ((c ^ sw) << 4)
 
-  // Rows past the end are not stored: those of packed operands read as zeros or
-  // as whatever row their offset wraps to, those of a 16-bit A repeat its last.
+  // Rows past the end are not stored: they read as zeros, or as whatever row a
+  // huge offset wraps to.
   const __amdgpu_buffer_rsrc_t rb = make_rsrc(a.B, a.b_bytes), rbs = make_rsrc(a.Bs, a.bs_bytes);
   const __amdgpu_buffer_rsrc_t ra = make_rsrc(a.A, a.a_bytes), ras = make_rsrc(a.As, a.as_bytes);
-  const uint8_t* A = static_cast<const uint8_t*>(a.A);
-  const uint32_t wrow = (n0 + lr) * a.G, mrow = (m0 + lr) * a.G;
-  uint32_t xrow[MB];
-#pragma unroll
-  for (int j = 0; j < MB; ++j) xrow[j] = min(m0 + 16 * j + lr, a.M - 1) * a.K;
+  const uint32_t wrow = (n0 + lr) * a.G, mrow = (m0 + lr) * (DTA == DT_MXFP4 ? a.G : a.K);
 
-  // this wave's groups of k: q0 .. q1 - 1
-  const uint32_t per = (a.G + NW - 1) / NW, q0 = min(w * per, a.G), q1 = min(q0 + per, a.G);
+  // this wave's units of k: d0 .. d1 - 1
+  const uint32_t units = (a.G + 1) >> 1, per = (units + NW - 1) / NW;
+  const uint32_t d0 = min(w * per, units), d1 = min(d0 + per, units);
 
-  // UN groups under way: codes of B, 16-byte pieces of A
-  constexpr int XC = DTA == DT_MXFP4 ? 1 : 4;
-  u32x4 wc[UN][NB], xc[UN][MB][XC];
-  auto load_w = [&](int u, uint32_t q) {
+  // under way: UN units of codes of B (and of A), XS pieces of a 16-bit A
+  constexpr int XC = DTA == DT_MXFP4 ? UN : XS;
+  u32x4 wc[UN][NB][2], xc[XC][MB][2];
+  // unit d of a packed operand; with an odd G the last one's second group is zero
+  auto load_packed = [&](__amdgpu_buffer_rsrc_t rs, uint32_t row, uint32_t d, auto& v) __attribute__((always_inline)) {
+    const bool cut = 2 * d + 1 >= a.G && lc >= 4;
 #pragma unroll
-    for (int i = 0; i < NB; ++i) wc[u][i] = ld_b128(rb, (wrow + (16u * i * a.G + q)) * 64u + 16u * lc);
+    for (int i = 0; i < (int)(sizeof(v) / sizeof(v[0])); ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        v[i][h] = ld_b128(rs, cut ? kOOB : (row + ((16u * i + 8u * h) * a.G + 2 * d)) * 64u + 16u * lc);
   };
-  // Piece c of A: values 128 q + 32 c + 8 lc .. + 7 of each row; where that runs
-  // past K (>= 8 for a 16-bit A), the row's last eight, shifted down on use.
-  auto load_x = [&](int u, int c, uint32_t q) {
-    if constexpr (DTA == DT_MXFP4) {
+  // Piece p of a 16-bit A: values 64 p + 8 lc .. + 7 of each row; where that runs
+  // past K (>= 8), the row's last eight, shifted down on use.  (A row need only be
+  // aligned for one value: the GPU runs with unaligned access on.)
+  auto load_x = [&](int slot, uint32_t p) __attribute__((always_inline)) {
+    const uint32_t k = min(p * 64u + lc * 8u, a.K - 8u);
 #pragma unroll
-      for (int j = 0; j < MB; ++j) xc[u][j][0] = ld_b128(ra, (mrow + (16u * j * a.G + q)) * 64u + 16u * lc);
-    } else {
-      const uint32_t k = min(q * 128u + c * 32u + lc * 8u, a.K - 8u);
+    for (int j = 0; j < MB; ++j)
 #pragma unroll
-      for (int j = 0; j < MB; ++j) xc[u][j][c] = mx::load_x8(A + (size_t)((xrow[j] + k) * 2u));
-    }
+      for (int h = 0; h < 2; ++h) xc[slot][j][h] = ld_b128(ra, (mrow + ((16u * j + 8u * h) * a.K + k)) * 2u);
   };
-  // Scale words of groups q .. q + 3 (none past the row's end): row n0 + lane of
-  // B for the first 16 NB lanes, and row m0 + lane of an MXFP4 A.
+  // Scale words of groups q .. q + 3 (zero past the row's end): row n0 + lane of B
+  // for the first 16 NB lanes, and row m0 + lane of an MXFP4 A.
   auto load_s = [&](__amdgpu_buffer_rsrc_t rs, uint32_t row, uint32_t q) {
     u32x4 v = {0, 0, 0, 0};
     const uint32_t at = (row * a.G + q) * 4u;
@@ -205,98 +200,123 @@ __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxGemmArgs a) {
 #pragma unroll
     for (int j = 0; j < MB; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // Adds group q's products from slot u and loads group q + UN into it.
-  auto multiply = [&](int u, uint32_t q) {
-    const bool more = q + UN < q1;                     // uniform
-    const uint32_t word = (q - q0) & 3u;               // of the scale words at hand
+  // Adds unit d's products from slot u and loads unit d + UN into it.
+  auto multiply = [&](int u, uint32_t d) __attribute__((always_inline)) {
+    const bool more = d + UN < d1;                     // uniform
+    const uint32_t word0 = ((d - d0) & 1u) * 2u;       // of the scale words at hand
     mx::lds_order();
-    if (word == 0) {
+    if (word0 == 0) {
       put_scales();
-      if (q + 4 < q1) load_scales(q + 4);
+      if (d + 2 < d1) load_scales(2 * d + 4);
     }
 #pragma unroll
-    for (int i = 0; i < NB; ++i) *reinterpret_cast<u32x4*>(my + W_AT + i * 1024 + put) = wc[u][i];
-    if (more) load_w(u, q + UN);
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) *reinterpret_cast<u32x4*>(my + W_AT + i * 2048 + h * 1024 + put) = wc[u][i][h];
+    if (more) load_packed(rb, wrow, d + UN, wc[u]);
     if constexpr (DTA == DT_MXFP4) {
 #pragma unroll
-      for (int j = 0; j < MB; ++j) *reinterpret_cast<u32x4*>(my + X_AT + j * 1024 + put) = xc[u][j][0];
-      if (more) load_x(u, 0, q + UN);
+      for (int j = 0; j < MB; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) *reinterpret_cast<u32x4*>(my + X_AT + j * 2048 + h * 1024 + put) = xc[u][j][h];
+      if (more) load_packed(ra, mrow, d + UN, xc[u]);
       mx::lds_order();
-      u32x4 xf[MB];
-      uint32_t sx[MB];
 #pragma unroll
-      for (int j = 0; j < MB; ++j) {
-        xf[j] = *reinterpret_cast<const u32x4*>(my + X_AT + j * 1024 + get + ((g ^ sw) << 4));
-        sx[j] = *reinterpret_cast<const uint32_t*>(my + S_AT + (TN + 16 * j + r) * 16 + word * 4) >> (8 * g);
-      }
+      for (int half = 0; half < 2; ++half) {           // (a missing second group adds zeros)
+        u32x4 xf[MB];
+        uint32_t sx[MB];
 #pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        const u32x4 wf = *reinterpret_cast<const u32x4*>(my + W_AT + i * 1024 + get + ((g ^ sw) << 4));
-        const uint32_t ws = *reinterpret_cast<const uint32_t*>(my + S_AT + (16 * i + r) * 16 + word * 4) >> (8 * g);
+        for (int j = 0; j < MB; ++j) {
+          xf[j] = *reinterpret_cast<const u32x4*>(my + X_AT + j * 2048 + get + (((4 * half + g) ^ sw) << 4));
+          sx[j] = *reinterpret_cast<const uint32_t*>(my + S_AT + (TN + 16 * j + r) * 16 + (word0 + half) * 4) >> (8 * g);
+        }
 #pragma unroll
-        for (int j = 0; j < MB; ++j) acc[i][j] = mx::mfma_mx(wf, xf[j], acc[i][j], ws, sx[j]);
+        for (int i = 0; i < NB; ++i) {
+          const u32x4 wf =
+              *reinterpret_cast<const u32x4*>(my + W_AT + i * 2048 + get + (((4 * half + g) ^ sw) << 4));
+          const uint32_t ws =
+              *reinterpret_cast<const uint32_t*>(my + S_AT + (16 * i + r) * 16 + (word0 + half) * 4) >> (8 * g);
+#pragma unroll
+          for (int j = 0; j < MB; ++j) acc[i][j] = mx::mfma_mx(wf, xf[j], acc[i][j], ws, sx[j]);
+        }
       }
     } else {
-      mx::lds_order();
-      uint32_t ws[NB];                                 // the four blocks' scale bytes of row 16 i + r
-      bool normal = true;
 #pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        ws[i] = *reinterpret_cast<const uint32_t*>(my + S_AT + (16 * i + r) * 16 + word * 4);
-        if constexpr (DTA == DT_F16)
+      for (int half = 0; half < 2; ++half) {
+        const uint32_t q = 2 * d + half;
+        if (half == 1 && q >= a.G) continue;           // uniform
+        mx::lds_order();
+        uint32_t ws[NB];                               // the four blocks' scale bytes of row 16 i + r
+        bool normal = true;
 #pragma unroll
-          for (int c = 0; c < 4; ++c)                  // (padding past K holds zeros, whatever its scale)
-            normal = normal && (((ws[i] >> (8 * c)) & 255u) - 114u <= 26u || q * 128u + c * 32u >= a.K);
-      }
-      if constexpr (DTA == DT_F16) normal = __all(normal);
+        for (int i = 0; i < NB; ++i) {
+          ws[i] = *reinterpret_cast<const uint32_t*>(my + S_AT + (16 * i + r) * 16 + (word0 + half) * 4);
+          if constexpr (DTA == DT_F16)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if ((q + 1) * 128u > a.K) {                    // uniform: the row ends in this group
-          const uint32_t k = q * 128u + c * 32u + lc * 8u;
-#pragma unroll
-          for (int j = 0; j < MB; ++j) xc[u][j][c] = mx::shift_x8(xc[u][j][c], k - min(k, a.K - 8u));
+            for (int c = 0; c < 4; ++c)                // (padding past K holds zeros, whatever its scale)
+              normal = normal && (((ws[i] >> (8 * c)) & 255u) - 114u <= 26u || q * 128u + c * 32u >= a.K);
         }
-        mx::lds_order();
+        if constexpr (DTA == DT_F16) normal = __all(normal);
 #pragma unroll
-        for (int j = 0; j < MB; ++j) *reinterpret_cast<u32x4*>(my + X_AT + j * 1024 + put) = xc[u][j][c];
-        if (more) load_x(u, c, q + UN);
-        mx::lds_order();
-        u32x4 xf[MB];
-        uint32_t wf[NB];                               // codes of the eight k from 8 g on
+        for (int pp = 0; pp < 2; ++pp) {
+          const int slot = XS == 2 ? pp : 4 * u + 2 * half + pp;
+          const uint32_t p = 2 * q + pp;
+          if ((q + 1) * 128u > a.K) {                  // uniform: the row ends in this group
+            const uint32_t k = p * 64u + lc * 8u, over = k - min(k, a.K - 8u);
 #pragma unroll
-        for (int i = 0; i < NB; ++i)
-          wf[i] = *reinterpret_cast<const uint32_t*>(my + W_AT + i * 1024 + get + ((c ^ sw) << 4) + 4 * g);
+            for (int j = 0; j < MB; ++j)
 #pragma unroll
-        for (int j = 0; j < MB; ++j)
-          xf[j] = *reinterpret_cast<const u32x4*>(my + X_AT + j * 1024 + get + ((g ^ sw) << 4));
-        auto field = [&](int i) { return __uint_as_float(((ws[i] >> (8 * c)) & 255u) << 23); };
-        if constexpr (DTA == DT_BF16) {
-#pragma unroll
-          for (int i = 0; i < NB; ++i) {
-            const u32x4 v = mx::decode_bf16(wf[i], field(i));
-#pragma unroll
-            for (int j = 0; j < MB; ++j) acc[i][j] = mx::mfma_bf16(v, xf[j], acc[i][j]);
+              for (int h = 0; h < 2; ++h) xc[slot][j][h] = mx::shift_x8(xc[slot][j][h], over);
           }
-        } else if (normal) {
+          mx::lds_order();
 #pragma unroll
-          for (int i = 0; i < NB; ++i) {
-            const u32x4 v = mx::decode_f16(wf[i], field(i));
+          for (int j = 0; j < MB; ++j)
 #pragma unroll
-            for (int j = 0; j < MB; ++j) acc[i][j] = mx::mfma_f16(v, xf[j], acc[i][j]);
-          }
-        } else {
+            for (int h = 0; h < 2; ++h)
+              *reinterpret_cast<u32x4*>(my + X_AT + j * 2048 + h * 1024 + put) = xc[slot][j][h];
+          if (p + XS < 4 * d1) load_x(slot, p + XS);
+          mx::lds_order();
 #pragma unroll
-          for (int i = 0; i < NB; ++i) {
-            const u32x4 v = mx::decode_f16(wf[i], 1.0f);
-            float s[4];                                // of the sums' rows, 16 i + 4 g + e
+          for (int cc = 0; cc < 2; ++cc) {
+            const int c = 2 * pp + cc;                 // block of the group
+            u32x4 xf[MB];
+            uint32_t wf[NB];                           // codes of the eight k from 8 g on
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              s[e] = mx::scale_value(my[S_AT + (16 * i + 4 * g + e) * 16 + word * 4 + c]);
+            for (int i = 0; i < NB; ++i)
+              wf[i] = *reinterpret_cast<const uint32_t*>(my + W_AT + i * 2048 + get + (((4 * half + c) ^ sw) << 4) + 4 * g);
 #pragma unroll
-            for (int j = 0; j < MB; ++j) {
-              const f32x4 z = mx::mfma_f16(v, xf[j], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+            for (int j = 0; j < MB; ++j)
+              xf[j] = *reinterpret_cast<const u32x4*>(my + X_AT + j * 2048 + get + (((4 * cc + g) ^ sw) << 4));
+            auto field = [&](int i) { return __uint_as_float(((ws[i] >> (8 * c)) & 255u) << 23); };
+            if constexpr (DTA == DT_BF16) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(z[e], s[e], acc[i][j][e]);
+              for (int i = 0; i < NB; ++i) {
+                const u32x4 v = mx::decode_bf16(wf[i], field(i));
+#pragma unroll
+                for (int j = 0; j < MB; ++j) acc[i][j] = mx::mfma_bf16(v, xf[j], acc[i][j]);
+              }
+            } else if (normal) {
+#pragma unroll
+              for (int i = 0; i < NB; ++i) {
+                const u32x4 v = mx::decode_f16(wf[i], field(i));
+#pragma unroll
+                for (int j = 0; j < MB; ++j) acc[i][j] = mx::mfma_f16(v, xf[j], acc[i][j]);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < NB; ++i) {
+                const u32x4 v = mx::decode_f16(wf[i], 1.0f);
+                float s[4];                            // of the sums' rows, 16 i + 4 g + e
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  s[e] = mx::scale_value(my[S_AT + (16 * i + 4 * g + e) * 16 + (word0 + half) * 4 + c]);
+#pragma unroll
+                for (int j = 0; j < MB; ++j) {
+                  const f32x4 z = mx::mfma_f16(v, xf[j], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(z[e], s[e], acc[i][j][e]);
+                }
+              }
             }
           }
         }
@@ -304,17 +324,22 @@ __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxGemmArgs a) {
     }
   };
 
-  // ---- the first groups of this wave -----------------------------------------------
-  if (q0 < q1) load_scales(q0);
+  // ---- the first units of this wave --------------------------------------------------
+  if (d0 < d1) load_scales(2 * d0);
 #pragma unroll
   for (int u = 0; u < UN; ++u)
-    if (q0 + u < q1) {
-      load_w(u, q0 + u);
-#pragma unroll
-      for (int c = 0; c < XC; ++c) load_x(u, c, q0 + u);
+    if (d0 + u < d1) {
+      load_packed(rb, wrow, d0 + u, wc[u]);
+      if constexpr (DTA == DT_MXFP4) load_packed(ra, mrow, d0 + u, xc[u]);
     }
+  if constexpr (DTA != DT_MXFP4) {
+#pragma unroll
+    for (int p = 0; p < XS; ++p)
+      if (4 * d0 + p < 4 * d1) load_x(p, 4 * d0 + p);
+  }
 
-  // ---- bias and residual of this thread's outputs, under the main loop ----------
+  // ---- bias and residual of this thread's outputs -----------------------------------
+  // under the main loop, or after it where that has no registers for them
   // quad o (four consecutive n of one row) of the tile, o = threadIdx.x + 64 NW p
   constexpr int QUADS = TM * TN / 4, P = (QUADS + 64 * NW - 1) / (64 * NW);
   const __amdgpu_buffer_rsrc_t rc = make_rsrc(a.C, a.c_bytes);
@@ -323,33 +348,38 @@ __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxGemmArgs a) {
                                     (4u * Elem<DTO>::bytes - 1u)) == 0;
   float add[P][4];
   uint32_t at[P];                                      // element offset of the quad, or kOOB
+  auto load_add = [&] {
 #pragma unroll
-  for (int p = 0; p < P; ++p) {
-    const uint32_t o = threadIdx.x + 64 * NW * p, ml = o / (TN / 4), nl = (o - ml * (TN / 4)) * 4;
-    const uint32_t m = m0 + ml, n = n0 + nl;
-    const bool in = o < (uint32_t)QUADS && m < a.M && n < a.N;
-    at[p] = in ? m * a.N + n : kOOB;
-    uint32_t idx[4] = {n, n + 1, n + 2, n + 3};
-    load_bias_vec<4>(a.bias, a.bias_bytes, a.bias_dt, idx, in ? a.N : 0u, add[p]);
-    if (a.R) {
-      float rv[4];
-      if (vec) {
-        load4<DTO>(rr, at[p], in, rv);
-      } else {
+    for (int p = 0; p < P; ++p) {
+      const uint32_t o = threadIdx.x + 64 * NW * p, ml = o / (TN / 4), nl = (o - ml * (TN / 4)) * 4;
+      const uint32_t m = m0 + ml, n = n0 + nl;
+      const bool in = o < (uint32_t)QUADS && m < a.M && n < a.N;
+      at[p] = in ? m * a.N + n : kOOB;
+      uint32_t idx[4] = {n, n + 1, n + 2, n + 3};
+      load_bias_vec<4>(a.bias, a.bias_bytes, a.bias_dt, idx, in ? a.N : 0u, add[p]);
+      if (a.R) {
+        float rv[4];
+        if (vec) {
+          load4<DTO>(rr, at[p], in, rv);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) rv[e] = load1<DTO>(rr, at[p] + e, in && n + e < a.N);
+          for (int e = 0; e < 4; ++e) rv[e] = load1<DTO>(rr, at[p] + e, in && n + e < a.N);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) add[p][e] += rv[e];
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) add[p][e] += rv[e];
     }
-  }
+  };
+  if constexpr (!LATE) load_add();
 
   // ---- main loop -------------------------------------------------------------------
-  for (uint32_t q = q0; q < q1; q += UN) {
+  for (uint32_t d = d0; d < d1; d += UN) {
 #pragma unroll
     for (int u = 0; u < UN; ++u)
-      if (q + u < q1) multiply(u, q + u);
+      if (d + u < d1) multiply(u, d + u);
   }
+
+  if constexpr (LATE) load_add();
 
   // ---- sums of the waves, epilogue ---------------------------------------------------
   // accumulator register e of lane (r, g): n = 16 i + 4 g + e, m = 16 j + r
@@ -415,13 +445,14 @@ inline void launch_mx_short(const MxGemmArgs& a, hipStream_t s) {
 
 template <int DTA, int DTO, int NB, int MB, int NW>
 inline void launch_mx_stream(MxGemmArgs a, hipStream_t s) {
-  // as many groups under way as leave room for the sums and the current one
-  constexpr int GROUP = 4 * NB + (DTA == DT_MXFP4 ? 4 : 16) * MB, LEFT = 150 - 4 * NB * MB;
-  constexpr int UN = 4 * GROUP <= LEFT ? 4 : 2 * GROUP <= LEFT ? 2 : 1;
+  // as many units under way as leave room for the sums and the current fragments;
+  // where not even one of a 16-bit A fits, two quarters of it
+  constexpr int UNIT = 8 * NB + (DTA == DT_MXFP4 ? 8 : 32) * MB, LEFT = 150 - 4 * NB * MB;
+  constexpr int UN = 4 * UNIT <= LEFT ? 4 : 2 * UNIT <= LEFT ? 2 : 1, XS = UNIT > LEFT ? 2 : 4 * UN;
   a.tiles_n = (a.N + 16 * NB - 1) / (16 * NB);
   a.tiles_m = (a.M + 16 * MB - 1) / (16 * MB);
   note_launch("gemm mxfp4 stream, %d n x %d m, k over %d waves", 16 * NB, 16 * MB, NW);
-  launch_kernel(mx_stream_kernel<DTA, DTO, NB, MB, NW, UN>, dim3(a.tiles_m * a.tiles_n), dim3(64 * NW), s, a);
+  launch_kernel(mx_stream_kernel<DTA, DTO, NB, MB, NW, UN, XS>, dim3(a.tiles_m * a.tiles_n), dim3(64 * NW), s, a);
 }
 
 }  // namespace biasact

@@ -19,9 +19,12 @@ inline void launch_mx_stream_nb(const MxGemmArgs& a, hipStream_t s) {
   auto cost = [&](uint32_t nb) {
     return (tiles_of(a, 16 * MB, 16 * nb) + 255) / 256 * (nb + (DTA == DT_MXFP4 ? 1 : 4) * MB + 2);
   };
-  const uint64_t c1 = cost(1), c2 = cost(2), c4 = cost(4);
-  if (c4 <= c2 && c4 <= c1) launch_mx_stream<DTA, DTO, 4, MB, 8>(a, s);
-  else if (c2 <= c1) launch_mx_stream<DTA, DTO, 2, MB, 8>(a, s);
+  const uint64_t c1 = cost(1), c2 = cost(2);
+  if constexpr (DTA != DT_F16 || MB < 4) {            // (fp16's second way leaves no registers for 4 x 4)
+    const uint64_t c4 = cost(4);
+    if (c4 <= c2 && c4 <= c1) return launch_mx_stream<DTA, DTO, 4, MB, 8>(a, s);
+  }
+  if (c2 <= c1) launch_mx_stream<DTA, DTO, 2, MB, 8>(a, s);
   else launch_mx_stream<DTA, DTO, 1, MB, 8>(a, s);
 }
 
