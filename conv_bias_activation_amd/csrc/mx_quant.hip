@@ -173,39 +173,71 @@ __global__ __launch_bounds__(256) void mx_dequantize_rows_kernel(MxQuantArgs a) 
 }
 
 // ---- blocks down the columns of X[K, rows] ----------------------------------
-// A lane holds one column's block of 32 k: consecutive lanes read consecutive
-// values of each row of X.  Wave w of the workgroup takes block w of a group
-// of 128, so the four waves fill a column's 64 bytes of codes.
-template <int DT>
-__global__ __launch_bounds__(256) void mx_quantize_cols_kernel(MxQuantArgs a) {
+// A workgroup takes two groups of 128 k of 64 CPL columns, wave w their block w:
+// a lane holds the block of its CPL columns, and consecutive lanes read
+// consecutive values of each row of X.  CPL = 2 for 16-bit types, four bytes a
+// load (an even number of columns, X aligned for them), else 1.  Codes and
+// scales leave through LDS (block b of column c at slot b ^ (c / 2 % 8), which
+// spreads a wave's writes over the banks), so that eight lanes store a
+// column's whole cache line of codes; from the registers each store would touch
+// 64 lines.  4096x4096 fp16 in 9.4 us, 13.8 without these two.
+template <int DT, int CPL>
+__global__ __launch_bounds__(512) void mx_quantize_cols_kernel(MxQuantArgs a) {
+  static_assert(CPL == 1 || Elem<DT>::bytes == 2, "two columns of a 16-bit type");
+  constexpr uint32_t COLS = 64 * CPL;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[COLS * 136];
   const uint32_t lane = threadIdx.x & 63u, blk = threadIdx.x >> 6;
-  const uint32_t g = fdiv(blockIdx.x, a.div_tiles), n = (blockIdx.x - g * a.div_tiles.div) * 64u + lane;
-  const uint32_t k0 = g * 128u + blk * 32u;
-  if (n >= a.rows) return;
-  Raw8<DT> v[4];
+  const uint32_t d = fdiv(blockIdx.x, a.div_tiles), n0 = (blockIdx.x - d * a.div_tiles.div) * COLS;
+  const uint32_t n = n0 + CPL * lane, k0 = d * 256u + blk * 32u;
+  const bool in = n < a.rows;
+  Raw8<DT> v[CPL][4];
 #pragma unroll
-  for (int q = 0; q < 4; ++q)
+  for (int c = 0; c < CPL; ++c)
 #pragma unroll
-    for (int i = 0; i < 2 * Elem<DT>::bytes; ++i) v[q].w[i] = 0;
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int i = 0; i < 2 * Elem<DT>::bytes; ++i) v[c][q].w[i] = 0;
+  uint32_t x[32];
 #pragma unroll
   for (uint32_t j = 0; j < 32; ++j) {
-    if (k0 + j < a.K) {
-      const size_t at = (size_t)(k0 + j) * a.rows + n;
-      if constexpr (Elem<DT>::bytes == 4) v[j >> 3].w[j & 7] = static_cast<const uint32_t*>(a.X)[at];
-      else v[j >> 3].w[(j & 7) >> 1] |= (uint32_t) static_cast<const uint16_t*>(a.X)[at] << (16 * (j & 1));
+    const size_t at = (size_t)(k0 + j) * a.rows + n;
+    const bool ok = in && k0 + j < a.K;
+    if constexpr (Elem<DT>::bytes == 4) x[j] = ok ? static_cast<const uint32_t*>(a.X)[at] : 0u;
+    else if constexpr (CPL == 2) x[j] = ok ? static_cast<const uint32_t*>(a.X)[at >> 1] : 0u;
+    else x[j] = ok ? static_cast<const uint16_t*>(a.X)[at] : 0u;
+  }
+#pragma unroll
+  for (uint32_t j = 0; j < 32; ++j) {
+    if constexpr (Elem<DT>::bytes == 4) {
+      v[0][j >> 3].w[j & 7] = x[j];
+    } else {
+      v[0][j >> 3].w[(j & 7) >> 1] |= (x[j] & 0xffffu) << (16 * (j & 1));
+      if constexpr (CPL == 2) v[1][j >> 3].w[(j & 7) >> 1] |= (x[j] >> 16) << (16 * (j & 1));
     }
   }
-  uint32_t m = 0;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) m = max(m, max_abs_bits<DT>(v[q]));
-  const uint32_t byte = scale_byte<DT>(m);
-  u32x4 o;
-  o.x = encode8<DT>(v[0], byte);
-  o.y = encode8<DT>(v[1], byte);
-  o.z = encode8<DT>(v[2], byte);
-  o.w = encode8<DT>(v[3], byte);
-  *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(a.codes) + ((size_t)n * a.G + g) * 64u + blk * 16u) = o;
-  static_cast<uint8_t*>(a.scales)[((size_t)n * a.G + g) * 4u + blk] = (uint8_t)byte;
+  for (int c = 0; c < CPL; ++c) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) m = max(m, max_abs_bits<DT>(v[c][q]));
+    const uint32_t byte = scale_byte<DT>(m), col = CPL * lane + c;
+    const u32x4 o = {encode8<DT>(v[c][0], byte), encode8<DT>(v[c][1], byte), encode8<DT>(v[c][2], byte),
+                     encode8<DT>(v[c][3], byte)};
+    *reinterpret_cast<u32x4*>(lds + col * 128u + ((blk ^ ((col >> 1) & 7u)) << 4)) = o;
+    lds[COLS * 128u + col * 8u + blk] = (uint8_t)byte;
+  }
+  __syncthreads();
+#pragma unroll
+  for (uint32_t c = threadIdx.x >> 3; c < COLS; c += 64) {
+    const uint32_t b = threadIdx.x & 7u;
+    if (n0 + c < a.rows && 2 * d + (b >> 2) < a.G)
+      *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(a.codes) + ((size_t)(n0 + c) * a.G + 2 * d) * 64u + b * 16u) =
+          *reinterpret_cast<const u32x4*>(lds + c * 128u + ((b ^ ((c >> 1) & 7u)) << 4));
+  }
+  const uint32_t c = threadIdx.x >> 1, half = threadIdx.x & 1u;
+  if (c < COLS && n0 + c < a.rows && 2 * d + half < a.G)
+    static_cast<uint32_t*>(a.scales)[(size_t)(n0 + c) * a.G + 2 * d + half] =
+        *reinterpret_cast<const uint32_t*>(lds + COLS * 128u + c * 8u + half * 4u);
 }
 
 template <int DT>
@@ -237,10 +269,16 @@ void launch(const MxQuantArgs& a, bool rows, bool back, hipStream_t s) {
     const dim3 grid((a.total + 255u) / 256u);
     if (back) launch_kernel(mx_dequantize_rows_kernel<DT>, grid, dim3(256), s, a);
     else launch_kernel(mx_quantize_rows_kernel<DT>, grid, dim3(256), s, a);
+  } else if (back) {
+    launch_kernel(mx_dequantize_cols_kernel<DT>, dim3(a.div_tiles.div * a.G), dim3(256), s, a);
   } else {
-    const dim3 grid(a.div_tiles.div * a.G);
-    if (back) launch_kernel(mx_dequantize_cols_kernel<DT>, grid, dim3(256), s, a);
-    else launch_kernel(mx_quantize_cols_kernel<DT>, grid, dim3(256), s, a);
+    constexpr int CPL = Elem<DT>::bytes == 2 ? 2 : 1;
+    const bool pairs = CPL == 2 && a.rows % 2 == 0 && (reinterpret_cast<uintptr_t>(a.X) & 3u) == 0;
+    MxQuantArgs b = a;
+    if (pairs) b.div_tiles = make_fastdiv((a.rows + 127u) / 128u);
+    const dim3 grid(b.div_tiles.div * ((a.G + 1u) / 2u));
+    if (pairs) launch_kernel(mx_quantize_cols_kernel<DT, CPL>, grid, dim3(512), s, b);
+    else launch_kernel(mx_quantize_cols_kernel<DT, 1>, grid, dim3(512), s, b);
   }
 }
 
