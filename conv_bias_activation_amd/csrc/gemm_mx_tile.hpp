@@ -152,11 +152,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx_tile_kernel(MxGemmArgs a) 
   const uint32_t a_rd = T::A_OFF + wm * 32 * SJ * 128 + fr, b_rd = T::B_OFF + wn * 32 * SI * 128 + fr;
 
   // ---- main loop ---------------------------------------------------------------------
-  // Step s: this wave's loads of it have landed; barrier; issue step s + 1 into
-  // the stage that s - 1 held (every wave had its fragments of s - 1 before it
-  // came to this barrier); read fragments and multiply.  Scale words of the
-  // next two steps are loaded in even steps and put in odd ones, into the
-  // buffer whose last readers came to the barrier before.
+  // Step s: quarters 0 .. 2 multiply while the next quarter's fragments are read.
+  // Then the one barrier, after this wave's loads of step s + 1 have landed and
+  // its reads of step s are done: from there on stage s + 1 may be read and
+  // stage s overwritten.  The first fragments of s + 1 and half the loads of
+  // s + 2 go out before quarter 3 multiplies, the other half before the next
+  // quarter: four loads a wave are what the address unit takes in one quarter,
+  // and more would hold up the reads behind them.  Scale words of the next two
+  // steps are loaded in even steps and put in odd ones, before the barrier that
+  // their readers pass.
   const int steps = (G + 1) >> 1;
   u32x4 snext[T::S_LOADS];
   // this tile's bias (zeros past N or without one): its bits now, fp32 into LDS later
@@ -172,59 +176,65 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx_tile_kernel(MxGemmArgs a) 
   if (threadIdx.x < T::BN)
     *reinterpret_cast<float*>(smem + T::BIAS_OFF + threadIdx.x * 4) =
         a.bias_dt == DT_F16 ? widen<DT_F16>(bias) : a.bias_dt == DT_BF16 ? widen<DT_BF16>(bias) : widen<DT_F32>(bias);
-  auto step = [&](int s, int odd) __attribute__((always_inline)) {
+  const uint32_t sc_rd = T::S_OFF + lrow * 16 + half * 4;
+  u32x4 fa[2][SJ], fb[2][SI];                          // by parity of the quarter
+  uint32_t wa[2][SJ], wb[2][SI];                       // scale words, by parity of the step
+  auto read = [&](int ks, int odd) __attribute__((always_inline)) {
+    uint32_t ar = a_rd, br = b_rd;
+    if constexpr (SJ * SI > 4) asm volatile("" : "+v"(ar), "+v"(br));   // no registers for each chunk's address
+#pragma unroll
+    for (int si = 0; si < SI; ++si)
+      fb[ks & 1][si] = *reinterpret_cast<const u32x4*>(smem + (br ^ (16u * ks)) + odd * T::B_STAGE + si * 4096);
+#pragma unroll
+    for (int sj = 0; sj < SJ; ++sj)
+      fa[ks & 1][sj] = *reinterpret_cast<const u32x4*>(smem + (ar ^ (16u * ks)) + odd * T::A_STAGE + sj * 4096);
+  };
+  auto read_scales = [&](int s, int odd) __attribute__((always_inline)) {
+    const uint8_t* sp = smem + sc_rd + ((s >> 1) & 1) * T::S_BUF + odd * 8;
+#pragma unroll
+    for (int si = 0; si < SI; ++si)
+      wb[odd][si] = *reinterpret_cast<const uint32_t*>(sp + (T::BM + wn * 32 * SI + si * 32) * 16);
+#pragma unroll
+    for (int sj = 0; sj < SJ; ++sj)
+      wa[odd][sj] = *reinterpret_cast<const uint32_t*>(sp + (wm * 32 * SJ + sj * 32) * 16);
+  };
+  auto multiply = [&](auto ks_c, int odd) __attribute__((always_inline)) {
+    constexpr int ks = decltype(ks_c)::value;
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int si = 0; si < SI; ++si)
+#pragma unroll
+      for (int sj = 0; sj < SJ; ++sj)
+        acc[si][sj] = mxt::mfma32<ks>(fb[ks & 1][si], fa[ks & 1][sj], acc[si][sj], wb[odd][si], wa[odd][sj]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto join = [&] {
     __builtin_amdgcn_s_waitcnt(mxt::wait_vm(0));
-    __builtin_amdgcn_s_waitcnt(mxt::WAIT_LGKM0);       // the scales this wave put
+    __builtin_amdgcn_s_waitcnt(mxt::WAIT_LGKM0);
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    const int S = s >> 1;
-    const uint8_t* sp = smem + T::S_OFF + (S & 1) * T::S_BUF + (2 * odd + half) * 4;
-    uint32_t wa[SJ], wb[SI];
-#pragma unroll
-    for (int si = 0; si < SI; ++si)
-      wb[si] = *reinterpret_cast<const uint32_t*>(sp + (T::BM + wn * 32 * SI + si * 32 + lrow) * 16);
-#pragma unroll
-    for (int sj = 0; sj < SJ; ++sj)
-      wa[sj] = *reinterpret_cast<const uint32_t*>(sp + (wm * 32 * SJ + sj * 32 + lrow) * 16);
-    u32x4 fa[2][SJ], fb[2][SI];
-    uint32_t ar = a_rd, br = b_rd;
-    if constexpr (SJ * SI > 4) asm volatile("" : "+v"(ar), "+v"(br));   // no registers for each chunk's address
-    auto read = [&](int ks) {
-#pragma unroll
-      for (int si = 0; si < SI; ++si)
-        fb[ks & 1][si] = *reinterpret_cast<const u32x4*>(smem + (br ^ (16u * ks)) + odd * T::B_STAGE + si * 4096);
-#pragma unroll
-      for (int sj = 0; sj < SJ; ++sj)
-        fa[ks & 1][sj] = *reinterpret_cast<const u32x4*>(smem + (ar ^ (16u * ks)) + odd * T::A_STAGE + sj * 4096);
-    };
-    auto multiply = [&](auto ks_c) __attribute__((always_inline)) {
-      constexpr int ks = decltype(ks_c)::value;
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int si = 0; si < SI; ++si)
-#pragma unroll
-        for (int sj = 0; sj < SJ; ++sj)
-          acc[si][sj] = mxt::mfma32<ks>(fb[ks & 1][si], fa[ks & 1][sj], acc[si][sj], wb[si], wa[sj]);
-      __builtin_amdgcn_sched_barrier(0);
-    };
-    // The next fragments' reads and a share of the next step's loads go out
-    // before each quarter's matrix instructions: all loads at once would hold up
-    // the reads behind them.
-    read(0);
-    if (odd == 0) load_scales(S + 1, false, snext);
-    read(1);
-    issue(s + 1, odd ^ 1, 0, (LOADS + 2) / 3);
-    multiply(std::integral_constant<int, 0>{});
-    read(2);
-    issue(s + 1, odd ^ 1, (LOADS + 2) / 3, 2 * ((LOADS + 2) / 3));
-    multiply(std::integral_constant<int, 1>{});
-    read(3);
-    issue(s + 1, odd ^ 1, 2 * ((LOADS + 2) / 3), LOADS);
-    if (odd == 1) put_scales(S + 1, snext);
-    multiply(std::integral_constant<int, 2>{});
-    multiply(std::integral_constant<int, 3>{});
   };
+  auto step = [&](int s, int odd) __attribute__((always_inline)) {
+    read(1, odd);
+    if (odd == 0) load_scales((s >> 1) + 1, false, snext);
+    issue(s + 1, odd ^ 1, LOADS / 2, LOADS);
+    multiply(std::integral_constant<int, 0>{}, odd);
+    read(2, odd);
+    multiply(std::integral_constant<int, 1>{}, odd);
+    read(3, odd);
+    if (odd == 1) put_scales((s >> 1) + 1, snext);
+    multiply(std::integral_constant<int, 2>{}, odd);
+    join();
+    read(0, odd ^ 1);                                  // (past the last step: whatever is there, unused)
+    read_scales(s + 1, odd ^ 1);
+    issue(s + 2, odd, 0, LOADS / 2);
+    multiply(std::integral_constant<int, 3>{}, odd);
+  };
+  join();
+  read(0, 0);
+  read_scales(0, 0);
+  issue(1, 1, 0, LOADS / 2);
   for (int s = 0; s < steps; s += 2) {
     step(s, 0);
     if (s + 1 < steps) step(s + 1, 1);

@@ -223,8 +223,26 @@ def test_epilogue(ba, kind, out, act):
         run_case(ba, M, N, 384, kind, out, act, ["f32", "f16", "bf16", None][(i + M) % 4], residual=(i + M) % 2 == 0)
 
 
+@pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("act,bias_dt,residual", [("none", None, True), ("leaky_relu", "bf16", False), ("gelu", "f32", False),
+                                                  ("gelu", "f16", True), ("tanh", "f32", True), ("sigmoid", None, False)])
+@pytest.mark.parametrize("M,N,tile", [(1100, 1160, "128 m x 128 n"), (1030, 1217, "128 m x 128 n"),
+                                      (2304, 4104, "256 m x 256 n"), (2305, 4099, "256 m x 256 n")])
+def test_epilogue_of_the_tiles(ba, M, N, tile, act, bias_dt, residual, out):
+    # rows of whole 16-byte stores and ragged ones, a last tile of one row
+    run_case(ba, M, N, 200, "mxfp4", out, act, bias_dt, residual)
+    assert tile in ba.last_tile_config()
+
+
+@pytest.mark.parametrize("K", [1, 128, 129, 256, 300, 512, 513, 640, 768, 1100, 1280, 1281, 1700])
+@pytest.mark.parametrize("M,N", [(1100, 1160), (2305, 4104)])
+def test_reduction_lengths_of_the_tiles(ba, M, N, K):
+    run_case(ba, M, N, K, "mxfp4", "f32", seed=3)
+    assert "tile" in ba.last_tile_config()
+
+
 @pytest.mark.parametrize("kind", ["mxfp4", "bf16", "f16"])
-@pytest.mark.parametrize("M,N,K", [(3, 70, 300), (130, 301, 260), (256, 512, 512)])
+@pytest.mark.parametrize("M,N,K", [(3, 70, 300), (130, 301, 260), (256, 512, 512), (1100, 1160, 300)])
 def test_operands_aligned_for_one_value(ba, kind, M, N, K):
     run_case(ba, M, N, K, kind, "bf16", "gelu", "bf16", residual=True, shift=1)
 
