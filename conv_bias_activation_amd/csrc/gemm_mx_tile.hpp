@@ -52,6 +52,27 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* l
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, off, 0, 0, 0);
 }
 
+// 16 bytes that this kernel touches once (cache policy "non-temporal")
+__device__ __forceinline__ u32x4 load_once(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 2);
+}
+__device__ __forceinline__ void store_once(__amdgpu_buffer_rsrc_t r, uint32_t off, u32x4 v) {
+  __builtin_amdgcn_raw_buffer_store_b128(v, r, off, 0, 2);
+}
+
+// narrow<DTO> of two values into one word, by one instruction
+template <int DTO>
+__device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+  if constexpr (DTO == DT_F16) {
+    asm("" : "+v"(lo), "+v"(hi));                      // as in narrow: fp32 first
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), f16x2));
+  } else {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), mx::bf16x2));
+  }
+}
+
 // acc += b . a^T over 64 k, scale byte KS of each word
 template <int KS>
 __device__ __forceinline__ f32x16 mfma32(u32x4 b, u32x4 a, f32x16 acc, uint32_t sb, uint32_t sa) {
@@ -257,23 +278,24 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx_tile_kernel(MxGemmArgs a) 
   auto slot = [](int r, int c) { return (uint32_t)(r * (T::BN * ES) + ((c ^ (r & (CPR - 1))) << 4)); };
   // f(LDS address, element offset in C, whether there is such an output), for
   // every chunk of the pass's rows, a row's chunks in neighbouring lanes
-  auto by_chunk = [&](int pass, auto&& f) __attribute__((always_inline)) {
-#pragma unroll 4
-    for (int it = 0; it < ROWS * CPR / T::THREADS; ++it) {
-      const int r = it * (T::THREADS / CPR) + tid / CPR, c = tid % CPR;
+  constexpr int CHUNKS = ROWS * CPR / T::THREADS;
+  auto by_chunk = [&](int pass, int from, int count, auto&& f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < count; ++i) {
+      const int r = (from + i) * (T::THREADS / CPR) + tid / CPR, c = tid % CPR;
       const uint32_t m = m0 + pass * ROWS + r, n = n0 + c * EPC;
-      f(slot(r, c), m * a.N + n, m < a.M && n < a.N);
+      f(i, slot(r, c), m * a.N + n, m < a.M && n < a.N);
     }
   };
-  // the same for every single output
-  auto by_output = [&](int pass, auto&& f) __attribute__((always_inline)) {
-    for (int it = 0; it < ROWS / (WM * WN); ++it)
+  // the same for every single output, a wave's 64 E of count rows at a time
+  constexpr int E = T::BN / 64;
+  auto by_output = [&](int pass, int from, int count, auto&& f) __attribute__((always_inline)) {
 #pragma unroll
-      for (int e = 0; e < T::BN / 64; ++e) {
-        const int r = it * (WM * WN) + w, c = (tid & 63) + 64 * e;
-        const uint32_t m = m0 + pass * ROWS + r, n = n0 + c;
-        f(slot(r, c / EPC) + (c % EPC) * ES, m * a.N + n, m < a.M && n < a.N);
-      }
+    for (int i = 0; i < count * E; ++i) {
+      const int r = (from + i / E) * (WM * WN) + w, c = (tid & 63) + 64 * (i % E);
+      const uint32_t m = m0 + pass * ROWS + r, n = n0 + c;
+      f(i, slot(r, c / EPC) + (c % EPC) * ES, m * a.N + n, m < a.M && n < a.N);
+    }
   };
 #pragma unroll 1
   for (int pass = 0; pass < PASSES; ++pass) {
@@ -281,15 +303,27 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx_tile_kernel(MxGemmArgs a) 
     const int row = tid & 31, four = 4 * ((tid >> 5) & 1);
     __syncthreads();                                   // the last k-step, or the previous pass, is read
     if (a.R) {
+      // eight or more loads at a time: a write to LDS waits for all earlier loads
       if (vec) {
-        by_chunk(pass, [&](uint32_t p, uint32_t at, bool ok) {
-          *reinterpret_cast<u32x4*>(smem + p) = ld_b128(rr, ok ? at * ES : kOOB);
-        });
+#pragma unroll 1
+        for (int from = 0; from < CHUNKS; from += 8) {
+          u32x4 v[8];
+          by_chunk(pass, from, 8, [&](int i, uint32_t, uint32_t at, bool ok) { v[i] = mxt::load_once(rr, ok ? at * ES : kOOB); });
+          by_chunk(pass, from, 8, [&](int i, uint32_t p, uint32_t, bool) { *reinterpret_cast<u32x4*>(smem + p) = v[i]; });
+        }
       } else {
-        by_output(pass, [&](uint32_t p, uint32_t at, bool ok) {
-          if constexpr (ES == 4) *reinterpret_cast<uint32_t*>(smem + p) = ld_b32(rr, ok ? at * ES : kOOB);
-          else *reinterpret_cast<uint16_t*>(smem + p) = ld_b16(rr, ok ? at * ES : kOOB);
-        });
+#pragma unroll 1
+        for (int from = 0; from < ROWS / (WM * WN); from += 4) {
+          uint32_t v[4 * E];
+          by_output(pass, from, 4, [&](int i, uint32_t, uint32_t at, bool ok) {
+            if constexpr (ES == 4) v[i] = ld_b32(rr, ok ? at * ES : kOOB);
+            else v[i] = ld_b16(rr, ok ? at * ES : kOOB);
+          });
+          by_output(pass, from, 4, [&](int i, uint32_t p, uint32_t, bool) {
+            if constexpr (ES == 4) *reinterpret_cast<uint32_t*>(smem + p) = v[i];
+            else *reinterpret_cast<uint16_t*>(smem + p) = (uint16_t)v[i];
+          });
+        }
       }
       __syncthreads();
     }
@@ -322,8 +356,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx_tile_kernel(MxGemmArgs a) 
                   u32x2 o;
 #pragma unroll
                   for (int e = 0; e < 2; ++e)
-                    o[e] = narrow<DTO>(mx::act<ACT, DTO>(z[2 * e], a.alpha)) |
-                           (narrow<DTO>(mx::act<ACT, DTO>(z[2 * e + 1], a.alpha)) << 16);
+                    o[e] = mxt::narrow2<DTO>(mx::act<ACT, DTO>(z[2 * e], a.alpha), mx::act<ACT, DTO>(z[2 * e + 1], a.alpha));
                   *reinterpret_cast<u32x2*>(p) = o;
                 } else {
                   if constexpr (decltype(res_c)::value) {
@@ -343,14 +376,18 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx_tile_kernel(MxGemmArgs a) 
     }
     __syncthreads();
     if (vec) {
-      by_chunk(pass, [&](uint32_t p, uint32_t at, bool ok) {
-        st_b128(rc, ok ? at * ES : kOOB, *reinterpret_cast<const u32x4*>(smem + p));
-      });
+#pragma unroll 1
+      for (int from = 0; from < CHUNKS; from += 8)
+        by_chunk(pass, from, 8, [&](int, uint32_t p, uint32_t at, bool ok) {
+          mxt::store_once(rc, ok ? at * ES : kOOB, *reinterpret_cast<const u32x4*>(smem + p));
+        });
     } else {
-      by_output(pass, [&](uint32_t p, uint32_t at, bool ok) {
-        if constexpr (ES == 4) st_b32(rc, ok ? at * ES : kOOB, *reinterpret_cast<const uint32_t*>(smem + p));
-        else st_b16(rc, ok ? at * ES : kOOB, *reinterpret_cast<const uint16_t*>(smem + p));
-      });
+#pragma unroll 1
+      for (int from = 0; from < ROWS / (WM * WN); from += 4)
+        by_output(pass, from, 4, [&](int, uint32_t p, uint32_t at, bool ok) {
+          if constexpr (ES == 4) st_b32(rc, ok ? at * ES : kOOB, *reinterpret_cast<const uint32_t*>(smem + p));
+          else st_b16(rc, ok ? at * ES : kOOB, *reinterpret_cast<const uint16_t*>(smem + p));
+        });
     }
   }
 }
