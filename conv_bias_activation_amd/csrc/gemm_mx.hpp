@@ -15,7 +15,7 @@
 // instruction's layout through LDS of its own, a row's 16-byte chunk c at slot
 // c ^ (row & 7) so that neither side meets a bank twice; a wave's LDS operations
 // run in order, so this needs no barrier.  A register is loaded anew, for the
-// unit that is UN further, as soon as it has gone to LDS.  Scale words come for
+// next unit or piece, as soon as it has gone to LDS.  Scale words come for
 // two units at a time, one row a lane.
 //   MXFP4 A: v_mfma_scale_f32_16x16x128, lane (r, g) with block g of row r and
 //     its scale (byte g of the word, shifted down).
@@ -109,9 +109,8 @@ __device__ __forceinline__ float act(float z, float alpha) {
 
 }  // namespace mx
 
-// NB, MB: blocks of 16 rows of B and A per wave; NW: waves along k; UN: units of
-// 256 k that a wave has under way; XS: pieces of 64 k of a 16-bit A (4 UN, or 2).
-template <int DTA, int DTO, int NB, int MB, int NW, int UN, int XS>
+// NB, MB: blocks of 16 rows of B and A per wave; NW: waves along k.
+template <int DTA, int DTO, int NB, int MB, int NW>
 __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxGemmArgs a) {
   constexpr int TN = 16 * NB, TM = 16 * MB;
   constexpr bool LATE = NB * MB == 16;                 // the widest block: every register counts
@@ -147,9 +146,11 @@ __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxGemmArgs a) {
   const uint32_t units = (a.G + 1) >> 1, per = (units + NW - 1) / NW;
   const uint32_t d0 = min(w * per, units), d1 = min(d0 + per, units);
 
-  // under way: UN units of codes of B (and of A), XS pieces of a 16-bit A
-  constexpr int XC = DTA == DT_MXFP4 ? UN : XS;
-  u32x4 wc[UN][NB][2], xc[XC][MB][2];
+  // Under way: a unit of B (and of an MXFP4 A), or two pieces of 64 k of a 16-bit A.
+  // More of them cost more than they hide, since a short product's time is largely
+  // that of fetching its code, which they unroll: with two units of B and eight
+  // pieces 17x4096x4096 (bf16) took 7.6 us, with one and four 6.8, so 6.1.
+  u32x4 wc[NB][2], xc[DTA == DT_MXFP4 ? 1 : 2][MB][2];
   // unit d of a packed operand; with an odd G the last one's second group is zero
   auto load_packed = [&](__amdgpu_buffer_rsrc_t rs, uint32_t row, uint32_t d, auto& v) __attribute__((always_inline)) {
     const bool cut = 2 * d + 1 >= a.G && lc >= 4;
@@ -200,9 +201,9 @@ __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxGemmArgs a) {
 #pragma unroll
     for (int j = 0; j < MB; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // Adds unit d's products from slot u and loads unit d + UN into it.
-  auto multiply = [&](int u, uint32_t d) __attribute__((always_inline)) {
-    const bool more = d + UN < d1;                     // uniform
+  // Adds unit d's products and loads the next one.
+  auto multiply = [&](uint32_t d) __attribute__((always_inline)) {
+    const bool more = d + 1 < d1;                      // uniform
     const uint32_t word0 = ((d - d0) & 1u) * 2u;       // of the scale words at hand
     mx::lds_order();
     if (word0 == 0) {
@@ -212,14 +213,14 @@ __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxGemmArgs a) {
 #pragma unroll
     for (int i = 0; i < NB; ++i)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) *reinterpret_cast<u32x4*>(my + W_AT + i * 2048 + h * 1024 + put) = wc[u][i][h];
-    if (more) load_packed(rb, wrow, d + UN, wc[u]);
+      for (int h = 0; h < 2; ++h) *reinterpret_cast<u32x4*>(my + W_AT + i * 2048 + h * 1024 + put) = wc[i][h];
+    if (more) load_packed(rb, wrow, d + 1, wc);
     if constexpr (DTA == DT_MXFP4) {
 #pragma unroll
       for (int j = 0; j < MB; ++j)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) *reinterpret_cast<u32x4*>(my + X_AT + j * 2048 + h * 1024 + put) = xc[u][j][h];
-      if (more) load_packed(ra, mrow, d + UN, xc[u]);
+        for (int h = 0; h < 2; ++h) *reinterpret_cast<u32x4*>(my + X_AT + j * 2048 + h * 1024 + put) = xc[0][j][h];
+      if (more) load_packed(ra, mrow, d + 1, xc[0]);
       mx::lds_order();
 #pragma unroll
       for (int half = 0; half < 2; ++half) {           // (a missing second group adds zeros)
@@ -241,7 +242,7 @@ __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxGemmArgs a) {
         }
       }
     } else {
-#pragma unroll
+#pragma unroll 1
       for (int half = 0; half < 2; ++half) {
         const uint32_t q = 2 * d + half;
         if (half == 1 && q >= a.G) continue;           // uniform
@@ -259,22 +260,21 @@ __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxGemmArgs a) {
         if constexpr (DTA == DT_F16) normal = __all(normal);
 #pragma unroll
         for (int pp = 0; pp < 2; ++pp) {
-          const int slot = XS == 2 ? pp : 4 * u + 2 * half + pp;
           const uint32_t p = 2 * q + pp;
           if ((q + 1) * 128u > a.K) {                  // uniform: the row ends in this group
             const uint32_t k = p * 64u + lc * 8u, over = k - min(k, a.K - 8u);
 #pragma unroll
             for (int j = 0; j < MB; ++j)
 #pragma unroll
-              for (int h = 0; h < 2; ++h) xc[slot][j][h] = mx::shift_x8(xc[slot][j][h], over);
+              for (int h = 0; h < 2; ++h) xc[pp][j][h] = mx::shift_x8(xc[pp][j][h], over);
           }
           mx::lds_order();
 #pragma unroll
           for (int j = 0; j < MB; ++j)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-              *reinterpret_cast<u32x4*>(my + X_AT + j * 2048 + h * 1024 + put) = xc[slot][j][h];
-          if (p + XS < 4 * d1) load_x(slot, p + XS);
+              *reinterpret_cast<u32x4*>(my + X_AT + j * 2048 + h * 1024 + put) = xc[pp][j][h];
+          if (p + 2 < 4 * d1) load_x(pp, p + 2);
           mx::lds_order();
 #pragma unroll
           for (int cc = 0; cc < 2; ++cc) {
@@ -325,17 +325,15 @@ __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxGemmArgs a) {
   };
 
   // ---- the first units of this wave --------------------------------------------------
-  if (d0 < d1) load_scales(2 * d0);
-#pragma unroll
-  for (int u = 0; u < UN; ++u)
-    if (d0 + u < d1) {
-      load_packed(rb, wrow, d0 + u, wc[u]);
-      if constexpr (DTA == DT_MXFP4) load_packed(ra, mrow, d0 + u, xc[u]);
+  if (d0 < d1) {
+    load_scales(2 * d0);
+    load_packed(rb, wrow, d0, wc);
+    if constexpr (DTA == DT_MXFP4) {
+      load_packed(ra, mrow, d0, xc[0]);
+    } else {
+      load_x(0, 4 * d0);
+      load_x(1, 4 * d0 + 1);
     }
-  if constexpr (DTA != DT_MXFP4) {
-#pragma unroll
-    for (int p = 0; p < XS; ++p)
-      if (4 * d0 + p < 4 * d1) load_x(p, 4 * d0 + p);
   }
 
   // ---- bias and residual of this thread's outputs -----------------------------------
@@ -373,11 +371,7 @@ __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxGemmArgs a) {
   if constexpr (!LATE) load_add();
 
   // ---- main loop -------------------------------------------------------------------
-  for (uint32_t d = d0; d < d1; d += UN) {
-#pragma unroll
-    for (int u = 0; u < UN; ++u)
-      if (d + u < d1) multiply(u, d + u);
-  }
+  for (uint32_t d = d0; d < d1; ++d) multiply(d);
 
   if constexpr (LATE) load_add();
 
@@ -445,14 +439,10 @@ inline void launch_mx_short(const MxGemmArgs& a, hipStream_t s) {
 
 template <int DTA, int DTO, int NB, int MB, int NW>
 inline void launch_mx_stream(MxGemmArgs a, hipStream_t s) {
-  // as many units under way as leave room for the sums and the current fragments;
-  // where not even one of a 16-bit A fits, two quarters of it
-  constexpr int UNIT = 8 * NB + (DTA == DT_MXFP4 ? 8 : 32) * MB, LEFT = 150 - 4 * NB * MB;
-  constexpr int UN = 4 * UNIT <= LEFT ? 4 : 2 * UNIT <= LEFT ? 2 : 1, XS = UNIT > LEFT ? 2 : 4 * UN;
   a.tiles_n = (a.N + 16 * NB - 1) / (16 * NB);
   a.tiles_m = (a.M + 16 * MB - 1) / (16 * MB);
   note_launch("gemm mxfp4 stream, %d n x %d m, k over %d waves", 16 * NB, 16 * MB, NW);
-  launch_kernel(mx_stream_kernel<DTA, DTO, NB, MB, NW, UN, XS>, dim3(a.tiles_m * a.tiles_n), dim3(64 * NW), s, a);
+  launch_kernel(mx_stream_kernel<DTA, DTO, NB, MB, NW>, dim3(a.tiles_m * a.tiles_n), dim3(64 * NW), s, a);
 }
 
 }  // namespace biasact
