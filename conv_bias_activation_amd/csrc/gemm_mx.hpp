@@ -25,6 +25,15 @@
 //     they become fp16 values with their scale while every scale in sight lies
 //     in 2^-13 .. 2^13 (0.5 and 6 times it are normal fp16 numbers); else each
 //     block's products are summed unscaled and scaled in fp32.
+//
+// Measured with N = K = 4096, bf16 outputs: two MXFP4 operands 4.4 us for 8 rows
+// of A and 5.6 for 64; a bf16 A 5.3 us for one row (9 MB, 1.9 us at 4.9 TB/s),
+// 9.8 for 64 and 15.5 for 256 (554 TFLOP/s).  With few rows that is a launch
+// (1.7 us for a trivial kernel), fetching the code, and the loads' latency; with
+// many, a CU's reads of A and B from L2 (640 KB for 256 rows, 4.8 us) and their
+// way through LDS (4.5 us), which the two waves of a SIMD overlap only in part.
+// Tiles of 64x64 that share no operand between waves need the fewest LDS bytes
+// per product; sixteen waves along k changed these times by 1 %.
 #pragma once
 
 #include "epilogue.hpp"
@@ -109,8 +118,9 @@ __device__ __forceinline__ float act(float z, float alpha) {
 
 }  // namespace mx
 
-// NB, MB: blocks of 16 rows of B and A per wave; NW: waves along k.
-template <int DTA, int DTO, int NB, int MB, int NW>
+// NB, MB: blocks of 16 rows of B and A per wave; NW: waves along k; UN: units of
+// 256 k that a wave has under way.
+template <int DTA, int DTO, int NB, int MB, int NW, int UN>
 __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxGemmArgs a) {
   constexpr int TN = 16 * NB, TM = 16 * MB;
   constexpr bool LATE = NB * MB == 16;                 // the widest block: every register counts
@@ -146,11 +156,9 @@ __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxGemmArgs a) {
   const uint32_t units = (a.G + 1) >> 1, per = (units + NW - 1) / NW;
   const uint32_t d0 = min(w * per, units), d1 = min(d0 + per, units);
 
-  // Under way: a unit of B (and of an MXFP4 A), or two pieces of 64 k of a 16-bit A.
-  // More of them cost more than they hide, since a short product's time is largely
-  // that of fetching its code, which they unroll: with two units of B and eight
-  // pieces 17x4096x4096 (bf16) took 7.6 us, with one and four 6.8, so 6.1.
-  u32x4 wc[NB][2], xc[DTA == DT_MXFP4 ? 1 : 2][MB][2];
+  // under way: UN units of codes of B (and of A), XS pieces of 64 k of a 16-bit A
+  constexpr int XS = 2 * UN, XC = DTA == DT_MXFP4 ? UN : XS;
+  u32x4 wc[UN][NB][2], xc[XC][MB][2];
   // unit d of a packed operand; with an odd G the last one's second group is zero
   auto load_packed = [&](__amdgpu_buffer_rsrc_t rs, uint32_t row, uint32_t d, auto& v) __attribute__((always_inline)) {
     const bool cut = 2 * d + 1 >= a.G && lc >= 4;
@@ -201,9 +209,9 @@ __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxGemmArgs a) {
 #pragma unroll
     for (int j = 0; j < MB; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // Adds unit d's products and loads the next one.
-  auto multiply = [&](uint32_t d) __attribute__((always_inline)) {
-    const bool more = d + 1 < d1;                      // uniform
+  // Adds unit d's products from slot u and loads unit d + UN into it.
+  auto multiply = [&](int u, uint32_t d) __attribute__((always_inline)) {
+    const bool more = d + UN < d1;                     // uniform
     const uint32_t word0 = ((d - d0) & 1u) * 2u;       // of the scale words at hand
     mx::lds_order();
     if (word0 == 0) {
@@ -213,14 +221,14 @@ __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxGemmArgs a) {
 #pragma unroll
     for (int i = 0; i < NB; ++i)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) *reinterpret_cast<u32x4*>(my + W_AT + i * 2048 + h * 1024 + put) = wc[i][h];
-    if (more) load_packed(rb, wrow, d + 1, wc);
+      for (int h = 0; h < 2; ++h) *reinterpret_cast<u32x4*>(my + W_AT + i * 2048 + h * 1024 + put) = wc[u][i][h];
+    if (more) load_packed(rb, wrow, d + UN, wc[u]);
     if constexpr (DTA == DT_MXFP4) {
 #pragma unroll
       for (int j = 0; j < MB; ++j)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) *reinterpret_cast<u32x4*>(my + X_AT + j * 2048 + h * 1024 + put) = xc[0][j][h];
-      if (more) load_packed(ra, mrow, d + 1, xc[0]);
+        for (int h = 0; h < 2; ++h) *reinterpret_cast<u32x4*>(my + X_AT + j * 2048 + h * 1024 + put) = xc[u][j][h];
+      if (more) load_packed(ra, mrow, d + UN, xc[u]);
       mx::lds_order();
 #pragma unroll
       for (int half = 0; half < 2; ++half) {           // (a missing second group adds zeros)
@@ -242,7 +250,7 @@ __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxGemmArgs a) {
         }
       }
     } else {
-#pragma unroll 1
+#pragma unroll UN
       for (int half = 0; half < 2; ++half) {
         const uint32_t q = 2 * d + half;
         if (half == 1 && q >= a.G) continue;           // uniform
@@ -260,21 +268,22 @@ __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxGemmArgs a) {
         if constexpr (DTA == DT_F16) normal = __all(normal);
 #pragma unroll
         for (int pp = 0; pp < 2; ++pp) {
+          const int slot = UN == 1 ? pp : 2 * half + pp;
           const uint32_t p = 2 * q + pp;
           if ((q + 1) * 128u > a.K) {                  // uniform: the row ends in this group
             const uint32_t k = p * 64u + lc * 8u, over = k - min(k, a.K - 8u);
 #pragma unroll
             for (int j = 0; j < MB; ++j)
 #pragma unroll
-              for (int h = 0; h < 2; ++h) xc[pp][j][h] = mx::shift_x8(xc[pp][j][h], over);
+              for (int h = 0; h < 2; ++h) xc[slot][j][h] = mx::shift_x8(xc[slot][j][h], over);
           }
           mx::lds_order();
 #pragma unroll
           for (int j = 0; j < MB; ++j)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-              *reinterpret_cast<u32x4*>(my + X_AT + j * 2048 + h * 1024 + put) = xc[pp][j][h];
-          if (p + 2 < 4 * d1) load_x(pp, p + 2);
+              *reinterpret_cast<u32x4*>(my + X_AT + j * 2048 + h * 1024 + put) = xc[slot][j][h];
+          if (p + XS < 4 * d1) load_x(slot, p + XS);
           mx::lds_order();
 #pragma unroll
           for (int cc = 0; cc < 2; ++cc) {
@@ -325,15 +334,17 @@ __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxGemmArgs a) {
   };
 
   // ---- the first units of this wave --------------------------------------------------
-  if (d0 < d1) {
-    load_scales(2 * d0);
-    load_packed(rb, wrow, d0, wc);
-    if constexpr (DTA == DT_MXFP4) {
-      load_packed(ra, mrow, d0, xc[0]);
-    } else {
-      load_x(0, 4 * d0);
-      load_x(1, 4 * d0 + 1);
+  if (d0 < d1) load_scales(2 * d0);
+#pragma unroll
+  for (int u = 0; u < UN; ++u)
+    if (d0 + u < d1) {
+      load_packed(rb, wrow, d0 + u, wc[u]);
+      if constexpr (DTA == DT_MXFP4) load_packed(ra, mrow, d0 + u, xc[u]);
     }
+  if constexpr (DTA != DT_MXFP4) {
+#pragma unroll
+    for (int p = 0; p < XS; ++p)
+      if (d0 < d1) load_x(p, 4 * d0 + p);              // (a unit has four pieces)
   }
 
   // ---- bias and residual of this thread's outputs -----------------------------------
@@ -371,7 +382,11 @@ __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxGemmArgs a) {
   if constexpr (!LATE) load_add();
 
   // ---- main loop -------------------------------------------------------------------
-  for (uint32_t d = d0; d < d1; ++d) multiply(d);
+  for (uint32_t d = d0; d < d1; d += UN) {
+#pragma unroll
+    for (int u = 0; u < UN; ++u)
+      if (d + u < d1) multiply(u, d + u);
+  }
 
   if constexpr (LATE) load_add();
 
@@ -437,12 +452,21 @@ inline void launch_mx_short(const MxGemmArgs& a, hipStream_t s) {
   launch_kernel(mx_short_kernel<DTA, DTO>, dim3((a.M * a.N + 255) / 256), dim3(256), s, a);
 }
 
-template <int DTA, int DTO, int NB, int MB, int NW>
+template <int DTA, int DTO, int NB, int MB>
 inline void launch_mx_stream(MxGemmArgs a, hipStream_t s) {
+  constexpr int NW = 8;
   a.tiles_n = (a.N + 16 * NB - 1) / (16 * NB);
   a.tiles_m = (a.M + 16 * MB - 1) / (16 * MB);
   note_launch("gemm mxfp4 stream, %d n x %d m, k over %d waves", 16 * NB, 16 * MB, NW);
-  launch_kernel(mx_stream_kernel<DTA, DTO, NB, MB, NW>, dim3(a.tiles_m * a.tiles_n), dim3(64 * NW), s, a);
+  const dim3 grid(a.tiles_m * a.tiles_n), block(64 * NW);
+  // Two units under way where a wave walks at least four, for which B comes in at
+  // the rate that its loads under way allow: one row by 4096x16384 (bf16) 13.4 us,
+  // with one unit 16.8.  A shorter product takes longer with two, which unroll the
+  // code that it has to fetch: 17x4096x4096 7.6 us with two, 6.6 with one.
+  if constexpr (NB * MB <= 2)
+    if (a.G >= 2 * NW * 4)
+      return launch_kernel(mx_stream_kernel<DTA, DTO, NB, MB, NW, 2>, grid, block, s, a);
+  launch_kernel(mx_stream_kernel<DTA, DTO, NB, MB, NW, 1>, grid, block, s, a);
 }
 
 }  // namespace biasact

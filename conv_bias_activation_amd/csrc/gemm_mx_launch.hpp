@@ -22,10 +22,10 @@ inline void launch_mx_stream_nb(const MxGemmArgs& a, hipStream_t s) {
   const uint64_t c1 = cost(1), c2 = cost(2);
   if constexpr (DTA != DT_F16 || MB < 4) {            // (fp16's second way leaves no registers for 4 x 4)
     const uint64_t c4 = cost(4);
-    if (c4 <= c2 && c4 <= c1) return launch_mx_stream<DTA, DTO, 4, MB, 8>(a, s);
+    if (c4 <= c2 && c4 <= c1) return launch_mx_stream<DTA, DTO, 4, MB>(a, s);
   }
-  if (c2 <= c1) launch_mx_stream<DTA, DTO, 2, MB, 8>(a, s);
-  else launch_mx_stream<DTA, DTO, 1, MB, 8>(a, s);
+  if (c2 <= c1) launch_mx_stream<DTA, DTO, 2, MB>(a, s);
+  else launch_mx_stream<DTA, DTO, 1, MB>(a, s);
 }
 
 template <int DTA, int DTO>

@@ -17,11 +17,22 @@
 // steps at once, through registers: fetched with each step they would touch
 // one cache line per row, as many as the codes do.
 //
-// Epilogue: each lane adds the bias, applies the activation to its own sums and puts the rounded values into LDS (16-byte chunk c of row r at
-// slot c ^ r, within the row), from where whole rows are stored, 16 bytes a lane.
-// A residual comes in the same way: whole rows into LDS, then each value to the
-// lane that holds its sum.  16-bit outputs take one pass, 32-bit ones a pass for
-// each wm.
+// Epilogue: each lane adds the bias, applies the activation to its own sums and
+// puts the rounded values into LDS (16-byte chunk c of row r at slot c ^ r, within
+// the row), from where whole rows are stored, 16 bytes a lane.  A residual comes in
+// the same way: whole rows into LDS, then each value to the lane that holds its
+// sum.  16-bit outputs take one pass, 32-bit ones a pass for each wm.  Both have
+// the non-temporal policy: 32768x4096x1024 with a residual 150 us, 172 without.
+//
+// Measured, 256x256 tiles, bf16 outputs: 4096^3 with GELU 47.2 us (2.9 PFLOP/s),
+// 40 without an activation; a step costs a round of tiles 1.9 us, 4.5 PFLOP/s,
+// where these instructions alone reach 6.1 on random operands (8.3 on zeros: it
+// is power that bounds them).  The rest of a round is its epilogue: 3.3 us for
+// the sums' way through LDS, 3 to 5 for 33 MB of outputs, 6 for GELU's
+// instructions.  32768x4096x1024 takes 125 us, eight rounds.  Workgroups that
+// walk over tiles, the next one's first loads ahead of the stores, took as long
+// (130 us), since a later load returns after all earlier stores; products of one
+// round took 1 us longer.
 #pragma once
 
 #include "epilogue.hpp"

@@ -128,7 +128,10 @@ __device__ __forceinline__ Raw8<DT> decode8(uint32_t codes, uint32_t byte) {
 
 // ---- blocks along the rows of X[rows, K] ------------------------------------
 // One lane per 8 values: four lanes make a block, sixteen a group of 128, and
-// lane 0 of the sixteen writes the group's four scale bytes as one word.
+// lane 0 of the sixteen writes the group's four scale bytes as one word.  Bound
+// by the bytes: 32768x4096 bf16 (340 MB) in 73.5 us, 4.6 TB/s where a copy of
+// 2 GiB reaches 4.9; 4096x4096 in 8.0 us; one row of 4096 in 1.5 us, a launch.
+// Read back, with the codes still in the caches, 56 and 1.5 us.
 template <int DT>
 __global__ __launch_bounds__(256) void mx_quantize_rows_kernel(MxQuantArgs a) {
   const uint32_t t = blockIdx.x * 256u + threadIdx.x;
@@ -180,7 +183,8 @@ __global__ __launch_bounds__(256) void mx_dequantize_rows_kernel(MxQuantArgs a) 
 // scales leave through LDS (block b of column c at slot b ^ (c / 2 % 8), which
 // spreads a wave's writes over the banks), so that eight lanes store a
 // column's whole cache line of codes; from the registers each store would touch
-// 64 lines.  4096x4096 fp16 in 9.4 us, 13.8 without these two.
+// 64 lines.  Bound by the bytes: 4096x4096 fp16 (42 MB, 8.7 us at 4.9 TB/s) in
+// 9.4 us, 13.8 without these two; read back in 10.2.
 template <int DT, int CPL>
 __global__ __launch_bounds__(512) void mx_quantize_cols_kernel(MxQuantArgs a) {
   static_assert(CPL == 1 || Elem<DT>::bytes == 2, "two columns of a 16-bit type");

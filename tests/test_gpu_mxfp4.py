@@ -242,6 +242,13 @@ def test_reduction_lengths_of_the_tiles(ba, M, N, K):
 
 
 @pytest.mark.parametrize("kind", ["mxfp4", "bf16", "f16"])
+@pytest.mark.parametrize("M,N,K", [(1, 33, 8064), (2, 17, 8065), (16, 40, 8192), (20, 33, 8449), (17, 64, 10240),
+                                   (5, 5000, 8200), (32, 20, 16384)])
+def test_long_reductions(ba, M, N, K, kind):
+    run_case(ba, M, N, K, kind, "f32", act="relu", seed=17)
+
+
+@pytest.mark.parametrize("kind", ["mxfp4", "bf16", "f16"])
 @pytest.mark.parametrize("M,N,K", [(3, 70, 300), (130, 301, 260), (256, 512, 512), (1100, 1160, 300)])
 def test_operands_aligned_for_one_value(ba, kind, M, N, K):
     run_case(ba, M, N, K, kind, "bf16", "gelu", "bf16", residual=True, shift=1)
