@@ -185,11 +185,9 @@ __device__ __forceinline__ float sigmoid_f32(float z) {
 // (csrc/fit_erfc.py, which also reports the float32 error: relative
 // 4e-7 on [0, 1], 2e-6 on [1, 4], 8e-6 on [4, 9], the last dominated by the
 // rounding of the exponent's argument).  erfc(-x) = 2 - erfc(x).
-// erfc_scaled gives erfc(|x|) for |x| = ax, times 2^64 where `tiny` comes back
-// true: below 2^-126 the product is formed at that size, so that whoever
-// scales it back (exactly) rounds once onto the subnormal grid (see exp2_f32).
-__device__ __forceinline__ float erfc_scaled(float ax, bool& tiny) {
+__device__ __forceinline__ float erfc_f32(float x) {
 #pragma clang fp contract(off)
+  const float ax = __builtin_fabsf(x);
   const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.5f, ax, 1.0f));
   float p = 1.449302137e-01f;
   p = __builtin_fmaf(p, t, -6.808272004e-01f);
@@ -202,15 +200,11 @@ __device__ __forceinline__ float erfc_scaled(float ax, bool& tiny) {
   p = __builtin_fmaf(p, t, 9.986327887e-01f);
   p = __builtin_fmaf(p, t, -1.265447974e+00f);
   const float e = __builtin_fmaf(-ax, ax, p);
+  // below 2^-126 the product is formed at 2^64 times its size, then scaled
+  // back exactly (see exp2_f32): one rounding onto the subnormal grid
   const float s = e * 1.442695041f;
-  tiny = s < -126.0f;
-  return t * __builtin_amdgcn_exp2f(tiny ? s + 64.0f : s);
-}
-
-__device__ __forceinline__ float erfc_f32(float x) {
-#pragma clang fp contract(off)
-  bool tiny;
-  float r = erfc_scaled(__builtin_fabsf(x), tiny);
+  const bool tiny = s < -126.0f;
+  float r = t * __builtin_amdgcn_exp2f(tiny ? s + 64.0f : s);
   r = tiny ? r * 0x1p-64f : r;
   return x < 0.0f ? 2.0f - r : r;
 }
@@ -221,42 +215,6 @@ __device__ __forceinline__ float erfc_f32(float x) {
 __device__ __forceinline__ float gelu_f32(float z) {
 #pragma clang fp contract(off)
   return 0.5f * z * erfc_f32(z * -0.7071067812f);
-}
-
-// GELU whose far negative tail is formed at 2^64 times its size and scaled back
-// at the very end: fp32 results below 2^-126 take one rounding onto the
-// subnormal grid (gelu_f32 rounds Phi there first and then scales that error
-// by z).
-__device__ __forceinline__ float gelu_f32_tail(float z) {
-#pragma clang fp contract(off)
-  bool tiny;
-  const float r = erfc_scaled(__builtin_fabsf(z * -0.7071067812f), tiny);
-  const float h = 0.5f * z;
-  const float neg = tiny ? (h * r) * 0x1p-64f : h * r;
-  return z > 0.0f ? h * (2.0f - (tiny ? 0.0f : r)) : neg;
-}
-
-// GELU for a result that is next rounded to fp16 or bf16:
-//   gelu(z) = max(z, 0) - |z| / 2 * erfc(|z| / sqrt 2),
-// the last factor as t * 2^(-z^2 log2(e) / 2 + Q(t)), t = 1 / (1 + 0.35 |z|), Q of
-// degree 5 (csrc/fit_erfc.py; relative error below 2^-17, 1.3e-5 with the
-// roundings).  The exponent carries 16 more and |z| / 2 that much less, so that
-// results down to bf16's subnormals round once; |z| is bounded so that an
-// infinity times zero stays out.  14 instructions and two transcendentals for
-// gelu_f32's 24 and two.
-__device__ __forceinline__ float gelu_f32_short(float z) {
-#pragma clang fp contract(off)
-  const float az = __builtin_fabsf(z);
-  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(az, 0.35f, 1.0f));
-  float q = 3.331241608e-01f;
-  q = __builtin_fmaf(q, t, -1.050401449e+00f);
-  q = __builtin_fmaf(q, t, 7.378793359e-01f);
-  q = __builtin_fmaf(q, t, 3.479329050e-01f);
-  q = __builtin_fmaf(q, t, 1.473684072e+00f);
-  q = __builtin_fmaf(q, t, 16.0f - 1.842209578e+00f);
-  const float e = __builtin_fmaf(z * z, -0.72134752f, q);
-  const float h = __builtin_fminf(az, 0x1p14f) * 0x1p-17f;
-  return __builtin_fmaxf(z, 0.0f) - h * (t * __builtin_amdgcn_exp2f(e));
 }
 
 // The activation in fp32 for an output of type DTO (tanh is evaluated to

@@ -8,7 +8,7 @@ half-line.  The coefficients here are this script's own least-squares fit of
 P(t) = ln(erfc(x) / t) + x^2 on Chebyshev nodes of t in [1/6, 1]
 (x in [0, 10]; past x = 10 erfc is below the float32 range); negative
 arguments use erfc(-x) = 2 - erfc(x).  Run it to reprint the constants used
-in device_common.hpp and the maximum relative error of the float32
+in device_common.hpp (and mx_act.hpp) and the maximum relative error of the float32
 evaluation (Horner with fused multiply-adds, exp through exp2) against
 scipy.special.erfc in float64.
 

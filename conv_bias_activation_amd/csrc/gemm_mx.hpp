@@ -38,6 +38,7 @@
 
 #include "epilogue.hpp"
 #include "launch_kernel.hpp"
+#include "mx_act.hpp"
 #include "mx_args.hpp"
 #include "mx_launch.hpp"
 #include "tile_map.hpp"
@@ -105,15 +106,6 @@ __device__ __forceinline__ u32x4 shift_x8(u32x4 v, uint32_t d) {
   v = two ? u32x4{v.y, v.z, v.w, 0u} : v;
   v = four ? u32x4{v.z, v.w, 0u, 0u} : v;
   return all ? u32x4{0u, 0u, 0u, 0u} : v;
-}
-
-// The activation for an output of type DTO: GELU to the accuracy that a 16-bit
-// output keeps, and with its subnormal tail for fp32.
-template <int ACT, int DTO>
-__device__ __forceinline__ float act(float z, float alpha) {
-  if constexpr (ACT == ACT_GELU && DTO == DT_F32) return gelu_f32_tail(z);
-  else if constexpr (ACT == ACT_GELU) return gelu_f32_short(z);
-  else return act_fn<ACT, DTO>(z, alpha);
 }
 
 }  // namespace mx
