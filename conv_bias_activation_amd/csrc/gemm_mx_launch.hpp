@@ -34,13 +34,14 @@ inline void launch_gemm_mx_to(const MxGemmArgs& a, hipStream_t s) {
   if constexpr (DTA == DT_MXFP4) {
     // Past one round of 64x64 blocks the tiled kernels are faster; between them
     // the rounds decide.  Measured at K = 4096 (us a round): 256 workgroups of
-    // 64x64 streaming 8.3, up to 256 of 128x128 14, 512 of them 26, 256 of
-    // 256x256 40.  E.g. 512x4096: 17.0 streaming, 13.5 with 128x128; 64x16384:
-    // 10.4 and 16.1; 6464x790x7221: 44.7 with 128x128, 57.9 with 256x256; 4096^3: 52
-    // and 41.
+    // 64x64 streaming 8.1, up to 256 of 128x128 15, 512 of them 24, 256 of
+    // 256x256 40.  E.g. 512x4096: 15.2 streaming, 12.6 with 128x128; 64x16384:
+    // 9.9 and 15.9; 6464x790x7221: 44.5 with 128x128, 54.8 with 256x256; 4096^3:
+    // 52.6 and 40.2.  (Two rounds of streaming win again where 128x128 tiles leave
+    // half of the CUs idle over a long k: 512x4096x16384 41.8 against 49.9.)
     if (tiles_of(a, 64, 64) > 256) {
       const uint64_t t128 = tiles_of(a, 128, 128);
-      const uint64_t small = t128 <= 256 ? 14 : (t128 + 511) / 512 * 26, large = (tiles_of(a, 256, 256) + 255) / 256 * 40;
+      const uint64_t small = t128 <= 256 ? 15 : (t128 + 511) / 512 * 24, large = (tiles_of(a, 256, 256) + 255) / 256 * 40;
       if (large < small) return launch_mx_tile<DTO, 2, 4, 4, 2>(a, s);
       return launch_mx_tile<DTO, 2, 2, 2, 2>(a, s);
     }
