@@ -32,14 +32,16 @@ template <int DTA, int DTO>
 inline void launch_gemm_mx_to(const MxGemmArgs& a, hipStream_t s) {
   if (a.K < (DTA == DT_MXFP4 ? 1u : 8u)) return launch_mx_short<DTA, DTO>(a, s);
   if constexpr (DTA == DT_MXFP4) {
-    // Past one round of 64x64 blocks the tiled kernels are faster; between them
-    // the rounds decide.  Measured at K = 4096 (us a round): 256 workgroups of
-    // 64x64 streaming 8.1, up to 256 of 128x128 15, 512 of them 24, 256 of
-    // 256x256 40.  E.g. 512x4096: 15.2 streaming, 12.6 with 128x128; 64x16384:
-    // 9.9 and 15.9; 6464x790x7221: 44.5 with 128x128, 54.8 with 256x256; 4096^3:
-    // 52.6 and 40.2.  (Two rounds of streaming win again where 128x128 tiles leave
-    // half of the CUs idle over a long k: 512x4096x16384 41.8 against 49.9.)
-    if (tiles_of(a, 64, 64) > 256) {
+    // Past one round of 64x64 blocks the tiled kernels are faster, but for two
+    // rounds over a long k, where 128x128 tiles leave half of the CUs idle (us,
+    // streaming and 128x128: 512x4096x4096 15.2 and 12.6, x6144 20.9 and 17.8, x8192
+    // 25.4 and 27.6, x16384 41.8 and 49.9; 192x8192x12288 32.0 and 38.2; three
+    // rounds, 700x4096x12288, 48.3 and 38.0; one round, 64x16384x4096, 9.9 and 15.9).
+    // Between the tiles their rounds decide, at K = 4096: up to 256 of 128x128 15 us,
+    // 512 of them 24, 256 of 256x256 40.  E.g. 6464x790x7221: 44.5 with 128x128, 54.8
+    // with 256x256; 4096^3: 52.6 and 40.2.
+    const uint64_t blocks = tiles_of(a, 64, 64);
+    if (blocks > (a.G < 64 ? 256 : 512)) {
       const uint64_t t128 = tiles_of(a, 128, 128);
       const uint64_t small = t128 <= 256 ? 15 : (t128 + 511) / 512 * 24, large = (tiles_of(a, 256, 256) + 255) / 256 * 40;
       if (large < small) return launch_mx_tile<DTO, 2, 4, 4, 2>(a, s);

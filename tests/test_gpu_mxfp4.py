@@ -243,7 +243,7 @@ def test_reduction_lengths_of_the_tiles(ba, M, N, K):
 
 @pytest.mark.parametrize("kind", ["mxfp4", "bf16", "f16"])
 @pytest.mark.parametrize("M,N,K", [(1, 33, 8064), (2, 17, 8065), (16, 40, 8192), (20, 33, 8449), (17, 64, 10240),
-                                   (5, 5000, 8200), (32, 20, 16384)])
+                                   (5, 5000, 8200), (32, 20, 16384), (520, 2100, 8200)])
 def test_long_reductions(ba, M, N, K, kind):
     run_case(ba, M, N, K, kind, "f32", act="relu", seed=17)
 
