@@ -21,7 +21,14 @@
 //     its scale (byte g of the word, shifted down).
 //   16-bit A: v_mfma_f32_16x16x32 c covers block c, lane (r, g) the eight k from
 //     8 g on.  For bf16 the codes become bf16 values with their scale, which is
-//     exact (two significant bits and bf16's fp32 exponent range).  For fp16
+//     exact (two significant bits and bf16's fp32 exponent range; the smallest,
+//     2^-128, is a subnormal, which the instruction takes) up to scale byte 252,
+//     where 6 times the scale is 1.5 * 2^127.  Past that (bytes 253 and 254, which
+//     the quantiser never writes) a value can be infinite, and then so is, or NaN,
+//     every sum of its row: a wave that ends with such sums and has such scales
+//     forms its sums anew, each block's products unscaled and then scaled in fp32.
+//     (The loop itself has no registers for a second way, and looking for the
+//     bytes in it took 1 to 2 % of the small products' time.)  For fp16
 //     they become fp16 values with their scale while every scale in sight lies
 //     in 2^-13 .. 2^13 (0.5 and 6 times it are normal fp16 numbers); else each
 //     block's products are summed unscaled and scaled in fp32.
@@ -380,6 +387,51 @@ __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxGemmArgs a) {
       if (d + u < d1) multiply(u, d + u);
   }
 
+  // ---- once more, block by block, where a scale was more than bf16 can take ----------
+  if constexpr (DTA == DT_BF16) {
+    float t = 0.0f;                                    // NaN with any sum that is not finite
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) t = __builtin_fmaf(acc[i][0][e], 0.0f, t);
+    uint32_t high = 0;                                 // bit 7 of a byte: a scale byte past 252
+    if (__builtin_expect(__any(t != 0.0f), 0)) {
+#pragma unroll 1
+      for (uint32_t q = 2 * d0; q < min(2 * d1, a.G); ++q)
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const uint32_t s = ld_b32(rbs, ((n0 + 16 * i + r) * a.G + q) * 4u);
+          high |= ((s & 0x7f7f7f7fu) + 0x03030303u) & s;   // from 253 on its lower bits reach 125 and bit 7 is set
+        }
+    }
+    if (__builtin_expect(__any((high & 0x80808080u) != 0), 0)) {
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int j = 0; j < MB; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+      for (uint32_t b = 8 * d0; b < min(8 * d1, 4 * a.G); ++b) {     // blocks of the row
+        const uint32_t k = b * 32u + g * 8u, from = min(k, a.K - 8u);
+        u32x4 xf[MB];
+#pragma unroll
+        for (int j = 0; j < MB; ++j) xf[j] = mx::shift_x8(ld_b128(ra, ((m0 + 16 * j + r) * a.K + from) * 2u), k - from);
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const u32x4 v = mx::decode_bf16(ld_b32(rb, (n0 + 16 * i + r) * a.G * 64u + b * 16u + g * 4u), 1.0f);
+          float s[4];                                  // of the sums' rows, 16 i + 4 g + e
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[e] = mx::scale_value(ld_b8(rbs, (n0 + 16 * i + 4 * g + e) * a.G * 4u + b));
+#pragma unroll
+          for (int j = 0; j < MB; ++j) {
+            const f32x4 z = mx::mfma_bf16(v, xf[j], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(z[e], s[e], acc[i][j][e]);
+          }
+        }
+      }
+    }
+  }
+
   if constexpr (LATE) load_add();
 
   // ---- sums of the waves, epilogue ---------------------------------------------------
@@ -424,11 +476,16 @@ __global__ __launch_bounds__(256) void mx_short_kernel(MxGemmArgs a) {
   const uint32_t m = at / a.N, n = at - m * a.N;
   float z = 0.0f;
   if constexpr (DTA != DT_MXFP4) {
+    // fp32 holds 6 times the scale up to byte 252: the last factor of 2 or 4 of
+    // bytes 253 and 254 comes after the product with x
+    const uint32_t byte = a.K ? static_cast<const uint8_t*>(a.Bs)[n * 4u] : 0u;     // (nothing there for no columns)
+    const bool high = byte == 253u || byte == 254u;
+    const float s = __uint_as_float((high ? 252u : byte) << 23), rest = byte == 253u ? 2.0f : 4.0f;
     for (uint32_t k = 0; k < a.K; ++k) {
       const float x = widen<DTA>(static_cast<const uint16_t*>(a.A)[m * a.K + k]);
       const uint32_t c = static_cast<const uint8_t*>(a.B)[n * 64u + (k >> 1)] >> (4 * (k & 1));
-      const float s = __uint_as_float((uint32_t) static_cast<const uint8_t*>(a.Bs)[n * 4u] << 23);
-      z += x * __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 0)[0];
+      const float v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 0)[0];
+      z = high ? __builtin_fmaf(x * v, rest, z) : __builtin_fmaf(x, v, z);
     }
   }
   if (a.bias_dt >= 0) z += load_bias(make_rsrc(a.bias, a.bias_bytes), a.bias_dt, n);
