@@ -47,12 +47,13 @@ __device__ __forceinline__ float gelu_tail(float z) {
 // the last factor as t * 2^(-z^2 log2(e) / 2 + Q(t)), t = 1 / (1 + 0.35 |z|), Q of
 // degree 5 (csrc/fit_erfc.py; relative error below 2^-17, 1.3e-5 with the
 // roundings).  The exponent carries 16 more and |z| / 2 that much less, so that
-// results down to bf16's subnormals round once; |z| is bounded so that an
-// infinity times zero stays out.  14 instructions and two transcendentals for
-// gelu_f32's 24 and two.
+// results down to bf16's subnormals round once.  A positive z is bounded, so that
+// infinity times zero stays out of gelu(inf) = inf; gelu(-inf) = -inf * 0 is NaN
+// as in gelu_f32 and gelu_tail, and a NaN comes in through z * z.  14 instructions
+// and two transcendentals for gelu_f32's 24 and two.
 __device__ __forceinline__ float gelu_short(float z) {
 #pragma clang fp contract(off)
-  const float az = __builtin_fabsf(z);
+  const float az = __builtin_fabsf(__builtin_fminf(z, 0x1p14f));
   const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(az, 0.35f, 1.0f));
   float q = 3.331241608e-01f;
   q = __builtin_fmaf(q, t, -1.050401449e+00f);
@@ -61,8 +62,7 @@ __device__ __forceinline__ float gelu_short(float z) {
   q = __builtin_fmaf(q, t, 1.473684072e+00f);
   q = __builtin_fmaf(q, t, 16.0f - 1.842209578e+00f);
   const float e = __builtin_fmaf(z * z, -0.72134752f, q);
-  const float h = __builtin_fminf(az, 0x1p14f) * 0x1p-17f;
-  return __builtin_fmaxf(z, 0.0f) - h * (t * __builtin_amdgcn_exp2f(e));
+  return __builtin_fmaxf(z, 0.0f) - (az * 0x1p-17f) * (t * __builtin_amdgcn_exp2f(e));
 }
 
 // The activation for an output of type DTO: GELU to the accuracy that a 16-bit
