@@ -126,10 +126,12 @@ lib = _load()
 
 def _load_native():
     """The C++ way from torch tensors to the MXFP4 calls (native_call.cpp), or
-    None where torch or the module is missing: the calls below then marshal
-    through ctypes."""
+    None where torch or the module is missing, or where the module does not
+    load (built for another torch or Python; a warning says why): the calls
+    below then marshal through ctypes, to the same entry points."""
     import importlib.machinery
     import importlib.util
+    import warnings
     path = os.path.join(_HERE, "_native.so")
     try:
         import torch  # noqa: F401  (its libraries have to be there first)
@@ -138,8 +140,14 @@ def _load_native():
     if not os.path.exists(path):
         return None
     loader = importlib.machinery.ExtensionFileLoader(__package__ + "._native", path)
-    m = importlib.util.module_from_spec(importlib.util.spec_from_loader(loader.name, loader))
-    loader.exec_module(m)
+    try:
+        m = importlib.util.module_from_spec(importlib.util.spec_from_loader(loader.name, loader))
+        loader.exec_module(m)
+    except ImportError as e:
+        warnings.warn(f"{path} does not load ({e}); the MXFP4 calls go through ctypes, which costs them up to "
+                      "3 us of host time. Rebuild with `python conv_bias_activation_amd/build.py`.", RuntimeWarning,
+                      stacklevel=2)
+        return None
     m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         lib.mxfp4_quantize, lib.mxfp4_dequantize, lib.gemm_mxfp4_bias_act, lib.gemm_mxfp4_bias_add_act)))
     return m
