@@ -6,7 +6,9 @@
 
 Every HIP translation unit is compiled for gfx950 only, with packed-fp32
 instructions disabled (-Xclang -target-feature -Xclang -packed-fp32-ops), in
-parallel, then linked into conv_bias_activation_amd/libbiasact.so.
+parallel, then linked into conv_bias_activation_amd/libbiasact.so.  Where torch
+is built for HIP, native_call.cpp becomes _native.so beside it; that one is
+optional.
 """
 from __future__ import annotations
 
@@ -24,6 +26,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libbiasact.so")
 NATIVE = os.path.join(PKG, "_native.so")     # torch tensors -> libbiasact.so in C++ (see native_call.cpp)
+NATIVE_STEP = "native_call.cpp"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -52,12 +55,14 @@ def _run(cmd):
 
 
 def native_command(out: str):
-    """The compiler call for the torch side, or None without torch (the C ABI
-    and the ctypes binding do without it)."""
+    """The compiler call for the torch side, or None without a torch for HIP
+    (the C ABI and the ctypes binding do without it)."""
     try:
         import torch
         from torch.utils import cpp_extension
     except ImportError:
+        return None
+    if torch.version.hip is None:
         return None
     import sysconfig
     inc = [f"-I{p}" for p in (*cpp_extension.include_paths(), sysconfig.get_paths()["include"],
@@ -83,13 +88,19 @@ def build(jobs: int | None = None, verbose: bool = False) -> str:
                             "-c", os.path.join(CSRC, src), "-o", obj], obj))
     native = native_command(NATIVE + ".tmp")
     if native:
-        steps.append(("native_call.cpp", native, None))
-    objs = []
+        steps.append((NATIVE_STEP, native, None))
+    objs, no_native = [], "no torch for HIP"
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
         futs = {ex.submit(_run, cmd): (name, obj) for name, cmd, obj in steps}
         for f in cf.as_completed(futs):
             name, obj = futs[f]
-            dt, warn = f.result()
+            try:
+                dt, warn = f.result()
+            except RuntimeError as e:
+                if name != NATIVE_STEP:
+                    raise
+                native, no_native = None, str(e)     # e.g. no headers of Python or torch
+                continue
             if verbose:
                 print(f"  compiled {name} in {dt:.1f}s", flush=True)
             if warn and verbose:
@@ -98,6 +109,10 @@ def build(jobs: int | None = None, verbose: bool = False) -> str:
                 objs.append(obj)
     if native:
         os.replace(NATIVE + ".tmp", NATIVE)
+    else:
+        if os.path.exists(NATIVE):                   # of an earlier build, perhaps for another library
+            os.remove(NATIVE)
+        print(f"{os.path.basename(NATIVE)} is not built, the MXFP4 calls will go through ctypes: {no_native}", flush=True)
     tmp = LIB + ".tmp"
     _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *sorted(objs)])
     os.replace(tmp, LIB)

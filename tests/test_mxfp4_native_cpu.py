@@ -1,5 +1,6 @@
 """The C++ way of the MXFP4 binding (_native.so) is an accelerator: the package
 works without it, and its status is the call's."""
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -45,3 +46,57 @@ def test_the_package_imports_beside_such_a_module(tmp_path):
                        cwd=tmp_path, capture_output=True, text=True, env={**os.environ, "PYTHONPATH": str(tmp_path)})
     assert r.returncode == 0, r.stderr
     assert r.stdout.split() == "((3, 128), (3, 8)) None".split()
+
+
+# ---- the build where the module cannot be had ----------------------------------------------
+
+@pytest.fixture
+def build(monkeypatch, tmp_path):
+    """build.py with an output folder of its own, a stale _native.so in it, and compiler calls that only write
+    their output."""
+    spec = importlib.util.spec_from_file_location("biasact_build_under_test", os.path.join(PKG, "build.py"))
+    b = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(b)
+    for name, at in (("BUILD", "objects"), ("LIB", "lib.so"), ("NATIVE", "_native.so")):
+        monkeypatch.setattr(b, name, str(tmp_path / at))
+    (tmp_path / "_native.so").write_text("stale")
+
+    def run(cmd):
+        if any(c.endswith("native_call.cpp") for c in cmd) and b.native_fails:
+            raise RuntimeError("build step failed: Python.h: No such file or directory")
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write("built")
+        return 0.0, ""
+
+    b.native_fails = False
+    monkeypatch.setattr(b, "_run", run)
+    return b
+
+
+def test_build_with_the_module(build):
+    with open(build.build()) as lib, open(build.NATIVE) as native:
+        assert lib.read() == native.read() == "built"
+
+
+@pytest.mark.parametrize("why", ["its compiler call fails", "torch is not for HIP", "no torch"])
+def test_build_without_the_module(build, monkeypatch, capsys, why):
+    if why == "its compiler call fails":
+        build.native_fails = True
+    elif why == "no torch":
+        monkeypatch.setitem(sys.modules, "torch", None)
+    else:
+        monkeypatch.setattr(torch.version, "hip", None)
+    with open(build.build()) as lib:
+        assert lib.read() == "built"
+    assert not os.path.exists(build.NATIVE)              # the stale one is gone
+    assert "_native.so is not built" in capsys.readouterr().out
+
+
+def test_build_still_fails_for_the_library(build, monkeypatch):
+    def run(cmd):
+        if any(c.endswith("plan_mx.cpp") for c in cmd):
+            raise RuntimeError("build step failed")
+        return 0.0, ""
+    monkeypatch.setattr(build, "_run", run)
+    with pytest.raises(RuntimeError):
+        build.build()
