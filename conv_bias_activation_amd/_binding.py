@@ -569,8 +569,12 @@ def mxfp4_quantize(X, codes, scales, axis: int = 1, stream=None):
     """Quantises X to MXFP4 with blocks of 32 along `axis`: the rows of
     X[rows, K] (axis 1) or the columns of X[K, rows] (axis 0).  codes and
     scales (uint8, mxfp4_shapes(rows, K)) are written and returned."""
-    if stream is None and _native is not None and _native.quantize(X, codes, scales, axis):
-        return codes, scales
+    if stream is None and _native is not None:
+        rc = _native.quantize(X, codes, scales, axis)
+        if rc is True:
+            return codes, scales
+        if rc:                                   # the library's status; False: not called
+            _check(rc, "mxfp4_quantize")
     rows, K, dt = _mx_quant_args(X, codes, scales, axis, "X")
     rc = lib.mxfp4_quantize(_dev(X, "X"), _dev(codes, "codes"), _dev(scales, "scales"), rows, K, axis,
                             dt, _stream(stream))
@@ -582,8 +586,12 @@ def mxfp4_quantize(X, codes, scales, axis: int = 1, stream=None):
 def mxfp4_dequantize(codes, scales, Y, axis: int = 1, stream=None):
     """The values that codes and scales stand for, in Y's type and in Y's
     layout ([rows, K] with axis 1, [K, rows] with axis 0)."""
-    if stream is None and _native is not None and _native.dequantize(Y, codes, scales, axis):
-        return Y
+    if stream is None and _native is not None:
+        rc = _native.dequantize(Y, codes, scales, axis)
+        if rc is True:
+            return Y
+        if rc:
+            _check(rc, "mxfp4_dequantize")
     rows, K, dt = _mx_quant_args(Y, codes, scales, axis, "Y")
     rc = lib.mxfp4_dequantize(_dev(codes, "codes"), _dev(scales, "scales"), _dev(Y, "Y"), rows, K, axis,
                               dt, _stream(stream))
@@ -615,9 +623,12 @@ def _gemm_mx_args(A, a_scales, B, b_scales, bias, C):
 def gemm_mxfp4_bias_act(A, a_scales, B, b_scales, bias, C, act="none", alpha: float = 0.0, stream=None):
     """C = act(A @ B.T + bias), B in MXFP4 (codes and b_scales of its N rows);
     A in MXFP4 (codes and a_scales), or fp16 / bf16 with a_scales None."""
-    if (stream is None and _native is not None
-            and _native.gemm(A, a_scales, B, b_scales, bias, None, C, act, alpha)):
-        return C
+    if stream is None and _native is not None:
+        rc = _native.gemm(A, a_scales, B, b_scales, bias, None, C, act, alpha)
+        if rc is True:
+            return C
+        if rc:
+            _check(rc, "gemm_mxfp4_bias_act")
     M, N, K, dt = _gemm_mx_args(A, a_scales, B, b_scales, bias, C)
     rc = lib.gemm_mxfp4_bias_act(_dev(A, "A"), _dev(a_scales, "a_scales"), _dev(B, "B"),
                                  _dev(b_scales, "b_scales"), _dev(bias, "bias"), _dev(C, "C"), M, N, K, dt,
@@ -630,9 +641,12 @@ def gemm_mxfp4_bias_act(A, a_scales, B, b_scales, bias, C, act="none", alpha: fl
 def gemm_mxfp4_bias_add_act(A, a_scales, B, b_scales, bias, R, C, act="none", alpha: float = 0.0,
                             stream=None):
     """C = act(A @ B.T + bias + R); R like C (may be C itself)."""
-    if (stream is None and _native is not None and R is not None
-            and _native.gemm(A, a_scales, B, b_scales, bias, R, C, act, alpha)):
-        return C
+    if stream is None and _native is not None and R is not None:
+        rc = _native.gemm(A, a_scales, B, b_scales, bias, R, C, act, alpha)
+        if rc is True:
+            return C
+        if rc:
+            _check(rc, "gemm_mxfp4_bias_add_act")
     M, N, K, dt = _gemm_mx_args(A, a_scales, B, b_scales, bias, C)
     rc = lib.gemm_mxfp4_bias_add_act(_dev(A, "A"), _dev(a_scales, "a_scales"), _dev(B, "B"),
                                      _dev(b_scales, "b_scales"), _dev(bias, "bias"), _residual(R, C),

@@ -3,10 +3,10 @@
 // checks and marshalling in Python take 1.6 us (quantise) to 3 us (product) of
 // host time beside a launch's 2 to 3, in C++ 0.1 to 0.2.
 //
-// Each function makes the call and returns True, or returns False without
-// having called anything when an argument is not what the call takes; the
-// binding then goes through its own checks, which say what is wrong.  It also
-// returns False where the library refused the call.
+// Each function makes the call and returns True, or the library's status where
+// that is not BA_OK; it returns False without having called anything when an
+// argument is not what the call takes, and the binding then goes through its own
+// checks, which say what is wrong.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -50,22 +50,23 @@ bool packed(const at::Tensor* c, const at::Tensor* s, int64_t* rows, int64_t* g)
   return s->size(1) % 4 == 0 && c->size(0) == *rows && c->size(1) == 64 * *g && on_device(*c) && on_device(*s);
 }
 
+constexpr int kNotTaken = -1;      // no call made; else the call's status
+
 hipStream_t current_stream() { return c10::hip::getCurrentHIPStream().stream(); }
 
 // (X, codes, scales, axis)
 template <bool BACK>
-bool quantize(PyObject* const* a) {
+int quantize(PyObject* const* a) {
   const at::Tensor *X = tensor(a[0]), *c = tensor(a[1]), *s = tensor(a[2]);
-  if (!X || !PyLong_CheckExact(a[3])) return false;
+  if (!X || !PyLong_CheckExact(a[3])) return kNotTaken;
   const long axis = PyLong_AsLong(a[3]);
   int64_t rows, g;
-  if ((axis != 0 && axis != 1) || X->dim() != 2 || !on_device(*X) || !packed(c, s, &rows, &g)) return false;
+  if ((axis != 0 && axis != 1) || X->dim() != 2 || !on_device(*X) || !packed(c, s, &rows, &g)) return kNotTaken;
   const int64_t xr = X->size(axis == 1 ? 0 : 1), K = X->size(axis == 1 ? 1 : 0);
   const int dt = float_code(*X);
-  if (xr != rows || (K + 127) / 128 != g || dt < 0) return false;
-  const int rc = BACK ? p_dequantize(c->data_ptr(), s->data_ptr(), X->data_ptr(), rows, K, (int)axis, dt, current_stream())
-                      : p_quantize(X->data_ptr(), c->data_ptr(), s->data_ptr(), rows, K, (int)axis, dt, current_stream());
-  return rc == BA_OK;
+  if (xr != rows || (K + 127) / 128 != g || dt < 0) return kNotTaken;
+  return BACK ? p_dequantize(c->data_ptr(), s->data_ptr(), X->data_ptr(), rows, K, (int)axis, dt, current_stream())
+              : p_quantize(X->data_ptr(), c->data_ptr(), s->data_ptr(), rows, K, (int)axis, dt, current_stream());
 }
 
 int act_code(PyObject* o) {
@@ -78,62 +79,60 @@ int act_code(PyObject* o) {
 }
 
 // (A, a_scales or None, B, b_scales, bias or None, R or None, C, act, alpha)
-bool gemm(PyObject* const* a) {
+int gemm(PyObject* const* a) {
   const at::Tensor *A = tensor(a[0]), *B = tensor(a[2]), *Bs = tensor(a[3]), *C = tensor(a[6]);
   const at::Tensor *As = nullptr, *bias = nullptr, *R = nullptr;
   int64_t M, N, K, g;
-  if (!A || !C || C->dim() != 2 || !packed(B, Bs, &N, &g)) return false;
+  if (!A || !C || C->dim() != 2 || !packed(B, Bs, &N, &g)) return kNotTaken;
   int ta = BA_MXFP4, tb = BA_F32;
   if (a[1] != Py_None) {
     int64_t ga;
     As = tensor(a[1]);
-    if (!packed(A, As, &M, &ga) || ga != g) return false;
+    if (!packed(A, As, &M, &ga) || ga != g) return kNotTaken;
     K = 128 * g;
   } else {
     ta = float_code(*A);
-    if (A->dim() != 2 || !on_device(*A) || (ta != BA_F16 && ta != BA_BF16)) return false;
+    if (A->dim() != 2 || !on_device(*A) || (ta != BA_F16 && ta != BA_BF16)) return kNotTaken;
     M = A->size(0);
     K = A->size(1);
-    if ((K + 127) / 128 != g) return false;
+    if ((K + 127) / 128 != g) return kNotTaken;
   }
   const int tc = float_code(*C);
-  if (tc < 0 || C->size(0) != M || C->size(1) != N || !on_device(*C)) return false;
+  if (tc < 0 || C->size(0) != M || C->size(1) != N || !on_device(*C)) return kNotTaken;
   if (a[4] != Py_None) {
     bias = tensor(a[4]);
-    if (!bias || bias->numel() != N || !on_device(*bias) || (tb = float_code(*bias)) < 0) return false;
+    if (!bias || bias->numel() != N || !on_device(*bias) || (tb = float_code(*bias)) < 0) return kNotTaken;
   }
   if (a[5] != Py_None) {
     R = tensor(a[5]);
-    if (!R || R->sizes() != C->sizes() || R->scalar_type() != C->scalar_type() || !on_device(*R)) return false;
+    if (!R || R->sizes() != C->sizes() || R->scalar_type() != C->scalar_type() || !on_device(*R)) return kNotTaken;
   }
   const int act = act_code(a[7]);
   const double alpha = PyFloat_CheckExact(a[8]) ? PyFloat_AS_DOUBLE(a[8]) : 0.0;
-  if (act < 0 || !PyFloat_CheckExact(a[8])) return false;
+  if (act < 0 || !PyFloat_CheckExact(a[8])) return kNotTaken;
   const uint32_t dt = BA_DTYPES(ta, BA_MXFP4, tb, tc);
   void* const as = As ? As->data_ptr() : nullptr;
   void* const bp = bias ? bias->data_ptr() : nullptr;
-  const int rc =
-      R ? p_gemm_add(A->data_ptr(), as, B->data_ptr(), Bs->data_ptr(), bp, R->data_ptr(), C->data_ptr(), M, N, K, dt,
-                     act, (float)alpha, current_stream())
-        : p_gemm(A->data_ptr(), as, B->data_ptr(), Bs->data_ptr(), bp, C->data_ptr(), M, N, K, dt, act, (float)alpha,
-                 current_stream());
-  return rc == BA_OK;
+  return R ? p_gemm_add(A->data_ptr(), as, B->data_ptr(), Bs->data_ptr(), bp, R->data_ptr(), C->data_ptr(), M, N, K,
+                        dt, act, (float)alpha, current_stream())
+           : p_gemm(A->data_ptr(), as, B->data_ptr(), Bs->data_ptr(), bp, C->data_ptr(), M, N, K, dt, act, (float)alpha,
+                    current_stream());
 }
 
 // No C++ exception reaches the interpreter: a call that throws is one that the
 // binding's own checks get to see.
-template <bool (*F)(PyObject* const*), Py_ssize_t N>
+template <int (*F)(PyObject* const*), Py_ssize_t N>
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  bool ok = false;
+  int rc = kNotTaken;
   if (p_quantize && n == N) {
     try {
-      ok = F(args);
+      rc = F(args);
     } catch (...) {
-      ok = false;
+      rc = kNotTaken;
     }
     if (PyErr_Occurred()) PyErr_Clear();
   }
-  return PyBool_FromLong(ok);
+  return rc == kNotTaken || rc == BA_OK ? PyBool_FromLong(rc == BA_OK) : PyLong_FromLong(rc);
 }
 
 // Addresses of the four entry points, in the order above.

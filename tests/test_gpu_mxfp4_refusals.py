@@ -2,6 +2,8 @@
 taken, with one argument changed at a time.  The C++ way must decline it without
 calling anything and the public call must raise; nothing is launched, so the
 outputs keep what was in them."""
+import ctypes
+
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -167,3 +169,30 @@ def test_alignment(ba, what):
         a[what] = off(8, 6, 128) if what == "B" else off(2, 6, 8)
         with pytest.raises(ValueError):
             ba.gemm_mxfp4_bias_add_act(*a.values())
+
+
+@pytest.mark.parametrize("status", [1, 2, 3])
+def test_the_status_of_a_call_that_fails(ba, status):
+    # entry points that only count and fail: one call each, its status comes back
+    B = ba._binding
+    names = ("mxfp4_quantize", "mxfp4_dequantize", "gemm_mxfp4_bias_act", "gemm_mxfp4_bias_add_act")
+    seen = []
+
+    def failing(name):
+        return ctypes.CFUNCTYPE(ctypes.c_int, *getattr(B.lib, name).argtypes)(lambda *a: seen.append(name) or status)
+
+    address = lambda f: ctypes.cast(f, ctypes.c_void_p).value  # noqa: E731
+    fakes = [failing(name) for name in names]
+    q = (z(5, 200), u8(5, 128), u8(5, 8), 1)
+    a = arguments("bf16")
+    try:
+        B._native.bind(*map(address, fakes))
+        got = [B._native.quantize(*q), B._native.dequantize(*q), B._native.gemm(*{**a, "R": None}.values()), B._native.gemm(*a.values())]
+        assert got == [status] * 4 and not any(g is True for g in got)
+        assert seen == list(names)
+        with pytest.raises(ba.BiasActError if status == 3 else ValueError):
+            ba.gemm_mxfp4_bias_add_act(*a.values())
+        assert len(seen) == 5
+    finally:
+        B._native.bind(*(address(getattr(B.lib, name)) for name in names))
+    assert B._native.gemm(*a.values()) is True

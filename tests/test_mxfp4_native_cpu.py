@@ -48,6 +48,34 @@ def test_the_package_imports_beside_such_a_module(tmp_path):
     assert r.stdout.split() == "((3, 128), (3, 8)) None".split()
 
 
+# ---- a call that the library refuses -------------------------------------------------------
+
+class Refuses:
+    """Takes the place of the C++ way: every call is made and fails."""
+    calls = 0
+
+    def quantize(self, *a):
+        self.calls += 1
+        return self.status
+
+    dequantize = gemm = quantize
+
+
+@pytest.mark.parametrize("status,error", [(B.BA_ERR_HIP, ba.BiasActError), (B.BA_ERR_INVALID, ValueError),
+                                          (B.BA_ERR_UNSUPPORTED, ValueError)])
+@pytest.mark.parametrize("name,nargs", [("mxfp4_quantize", 3), ("mxfp4_dequantize", 3), ("gemm_mxfp4_bias_act", 6),
+                                        ("gemm_mxfp4_bias_add_act", 7)])
+def test_a_failed_call_is_not_made_again(monkeypatch, name, nargs, status, error):
+    n = Refuses()
+    n.status = status
+    monkeypatch.setattr(B, "_native", n)
+    with pytest.raises(error, match=name + ": ") as e:
+        getattr(ba, name)(*[object()] * nargs)           # the Python checks, which come before a second call, would trip
+    assert n.calls == 1
+    if error is ba.BiasActError:
+        assert e.value.status == status
+
+
 # ---- the build where the module cannot be had ----------------------------------------------
 
 @pytest.fixture
