@@ -394,14 +394,15 @@ __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxGemmArgs a) {
     for (int i = 0; i < NB; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) t = __builtin_fmaf(acc[i][0][e], 0.0f, t);
-    uint32_t high = 0;                                 // bit 7 of a byte: a scale byte past 252
+    uint32_t high = 0;                                 // bit 7 of a byte: a scale byte was 253 or 254
     if (__builtin_expect(__any(t != 0.0f), 0)) {
 #pragma unroll 1
       for (uint32_t q = 2 * d0; q < min(2 * d1, a.G); ++q)
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
           const uint32_t s = ld_b32(rbs, ((n0 + 16 * i + r) * a.G + q) * 4u);
-          high |= ((s & 0x7f7f7f7fu) + 0x03030303u) & s;   // from 253 on its lower bits reach 125 and bit 7 is set
+          // from 253 on a byte's lower bits reach 125 and bit 7 is set; 255 (NaN) has both low bits
+          high |= ((s & 0x7f7f7f7fu) + 0x03030303u) & s & ~((s << 7) & (s << 6));
         }
     }
     if (__builtin_expect(__any((high & 0x80808080u) != 0), 0)) {

@@ -101,3 +101,24 @@ def test_two_mxfp4_operands_of_opposite_scales(ba, large, M, N, K):
     C = torch.empty((M, N), device="cuda")
     ba.gemm_mxfp4_bias_act(dev(lo[0]), dev(lo[1]), dev(hi[0]), dev(hi[1]), None, C)
     check(C, mx.values(*lo, K), mx.values(*hi, K))
+
+
+@pytest.mark.parametrize("kind", ["mxfp4", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(9, 40, 1100), (40, 8192, 260), (1100, 1160, 300)])
+def test_a_nan_block_leaves_the_other_columns_bits(ba, kind, M, N, K):
+    # byte 255 is what the quantiser writes for a block with an infinity or a NaN
+    rng = np.random.default_rng(M)
+    if kind == "mxfp4":
+        A, As = map(dev, mx.random_packed(rng, M, K))
+    else:
+        A, As = dev(rng.standard_normal((M, K)), kind), None
+    c, s = mx.random_packed(rng, N, K)
+    want, got = torch.empty((M, N), device="cuda"), torch.empty((M, N), device="cuda")
+    ba.gemm_mxfp4_bias_act(A, As, dev(c), dev(s), None, want)
+    rows = [5, 21]
+    s[5, 0], s[21, K // 64] = 255, 255
+    ba.gemm_mxfp4_bias_act(A, As, dev(c), dev(s), None, got)
+    keep = torch.ones(N, dtype=torch.bool, device="cuda")
+    keep[rows] = False
+    assert bool(got[:, rows].isnan().all())
+    assert torch.equal(got[:, keep], want[:, keep])
