@@ -209,7 +209,7 @@ int conv2d_bias_add_act_2k(const void* x, const void* w, const void* bias, const
  *   codes  [rows, 64 * ceil(K / 128)] bytes, k even in a byte's low four bits,
  *   scales [rows,  4 * ceil(K / 128)] bytes,
  * i.e. each row is padded to whole groups of 128 values; the padding must be
- * zero codes (mxfp4_quantize writes it so, with scale bytes of zero).  codes
+ * zero codes, with scale bytes other than 255 (mxfp4_quantize writes zeros).  codes
  * must be 16-byte and scales 4-byte aligned (BA_ERR_INVALID otherwise).
  *
  * mxfp4_packed_size: bytes of the two arrays (host pointers). */
@@ -238,8 +238,9 @@ int mxfp4_dequantize(const void* codes, const void* scales, void* Y, int64_t row
  * fp16 / bf16 [M,K] with a_scales NULL.  bias and out: fp32, fp16 or bf16
  * each; R has C's type and shape and may be C itself.  The products are exact
  * (a 16-bit A's values are not rounded further), the sum, bias, residual and
- * activation run in fp32 with one rounding to C; the sum's order depends on
- * the sizes only, so equal calls give equal bits.  M, N, K >= 0 (M or N == 0:
+ * activation run in fp32 with one rounding to C.  The sum's order depends on
+ * the sizes and, with a 16-bit A, on which scales B holds, so equal calls give
+ * equal bits.  M, N, K >= 0 (M or N == 0:
  * nothing to do; K == 0: C = act(bias (+ R))).  Checks, limits and return
  * codes otherwise as gemm_bias_act / gemm_bias_add_act; the forced tile
  * configuration does not apply. */

@@ -122,3 +122,21 @@ def test_a_nan_block_leaves_the_other_columns_bits(ba, kind, M, N, K):
     keep[rows] = False
     assert bool(got[:, rows].isnan().all())
     assert torch.equal(got[:, keep], want[:, keep])
+
+
+@pytest.mark.parametrize("kind", ["mxfp4", "bf16", "f16"])
+@pytest.mark.parametrize("M,N,K", [(3, 48, 300), (40, 70, 130), (1100, 1160, 300), (3, 33, 7)])
+def test_scales_of_the_padding_do_not_matter(ba, kind, M, N, K):
+    # zero codes past K with any scale but NaN
+    rng = np.random.default_rng(M + K)
+    packed = [mx.random_packed(rng, rows, K) for rows in (N, M)]
+    A = None if kind == "mxfp4" else dev(rng.standard_normal((M, K)), kind)
+    got = []
+    for fill in (None, 1, 253, 254):
+        for _, s in packed:
+            s[:, -(-K // 32):] = 0 if fill is None else fill
+        (b, bs), (a, a_s) = packed
+        C = torch.empty((M, N), device="cuda")
+        ba.gemm_mxfp4_bias_act(dev(a) if A is None else A, dev(a_s) if A is None else None, dev(b), dev(bs), None, C)
+        got.append(C)
+    assert all(torch.equal(got[0], c) for c in got[1:])
