@@ -31,7 +31,10 @@
 //     bytes in it took 1 to 2 % of the small products' time.)  For fp16
 //     they become fp16 values with their scale while every scale in sight lies
 //     in 2^-13 .. 2^13 (0.5 and 6 times it are normal fp16 numbers); else each
-//     block's products are summed unscaled and scaled in fp32.
+//     block's products are summed unscaled and scaled in fp32.  In sight are the
+//     scales of the wave's rows in a group; byte 0, of a block of zeros or read for
+//     rows past N, takes the second way too: 1x4096x4096 5.8 us, 6.6 with one zero
+//     block in a thousand, 1x4095x4096 7.3 (64 rows: 9.9, 11.0 and 12.0).
 //
 // Measured with N = K = 4096, bf16 outputs: two MXFP4 operands 4.4 us for 8 rows
 // of A and 5.6 for 64; a bf16 A 5.3 us for one row (9 MB, 1.9 us at 4.9 TB/s),

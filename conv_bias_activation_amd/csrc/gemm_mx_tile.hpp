@@ -8,8 +8,11 @@
 // 68 against 133 GB/s measured from L2.)
 //
 // Codes reach LDS without passing through registers, 16 bytes a lane, two
-// stages deep; chunk c of row r lies at slot c ^ (r & 7), so the eight lanes
-// that a 16-byte LDS read serves at a time are on different banks.  The four
+// stages deep; chunk c of row r lies at slot c ^ (r & 7), which spreads the same
+// chunk of eight neighbouring rows over all slots.  Rows 8 apart share a slot, and
+// the counters show 4.5 conflict cycles per LDS instruction: reads of such
+// fragments and nothing else reach 285 B/ns a CU, 318 with slot c ^ ((r >> 1) & 7),
+// 321 in a row.  The four
 // v_mfma_scale_f32_32x32x64 of a step take chunk ks of the step's first group in
 // the lower half of a wave and chunk ks of its second group in the upper half:
 // each lane then needs one scale word per row and step, whose byte ks the
@@ -26,8 +29,8 @@
 //
 // Measured, 256x256 tiles, bf16 outputs: 4096^3 with GELU 47.2 us (2.9 PFLOP/s),
 // 40 without an activation; a step costs a round of tiles 1.9 us, 4.5 PFLOP/s,
-// where these instructions alone reach 6.1 on random operands (8.3 on zeros: it
-// is power that bounds them).  The rest of a round is its epilogue: 3.3 us for
+// where these instructions alone reach 5.6 to 6.1 on random operands (8.3 to 8.6 on
+// zeros: it is power that bounds them).  The rest of a round is its epilogue: 3.3 us for
 // the sums' way through LDS, 3 to 5 for 33 MB of outputs, 6 for GELU's
 // instructions.  32768x4096x1024 takes 125 us, eight rounds.  Workgroups that
 // walk over tiles, the next one's first loads ahead of the stores, took as long

@@ -184,7 +184,10 @@ __global__ __launch_bounds__(256) void mx_dequantize_rows_kernel(MxQuantArgs a) 
 // spreads a wave's writes over the banks), so that eight lanes store a
 // column's whole cache line of codes; from the registers each store would touch
 // 64 lines.  Bound by the bytes: 4096x4096 fp16 (42 MB, 8.7 us at 4.9 TB/s) in
-// 9.4 us, 13.8 without these two; read back in 10.2.
+// 9.4 us, 13.8 without these two; read back in 10.2.  With one column a lane, in
+// graph replay: 4096x4096 fp32 12.8 us (15.7 for the bytes from HBM) and
+// 16384x8192 fp32 125 (125), but a 16-bit X of odd width reads two bytes a lane:
+// 4095x4096 fp16 12.8 us where 4096x4096 takes 8.0, 16383x8192 bf16 87 for 76.
 template <int DT, int CPL>
 __global__ __launch_bounds__(512) void mx_quantize_cols_kernel(MxQuantArgs a) {
   static_assert(CPL == 1 || Elem<DT>::bytes == 2, "two columns of a 16-bit type");
