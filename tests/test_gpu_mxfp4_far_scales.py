@@ -32,9 +32,10 @@ def check(C, av, bv):
     assert (np.abs(got - ref) <= tol).all(), (np.isnan(got).sum(), np.isinf(got).sum())
 
 
-# blocks of 16 n x 16 m of the streaming kernel: 1x1, 1x2, 1x4, 2x4 and 4x4, one and two units under way, rows of fewer
-# than eight values
-SIZES = [(3, 48, 300), (20, 48, 300), (40, 70, 300), (40, 8192, 260), (64, 16384, 260), (2, 40, 8200), (3, 33, 7), (2, 5, 1)]
+# blocks of 16 n x 16 m of the streaming kernel: 1x1, 1x2, 1x4, 2x4, 4x4, 4x1 and 4x2, one unit under way and two, rows of
+# fewer than eight values
+SIZES = [(3, 48, 300), (20, 48, 300), (40, 70, 300), (40, 8192, 260), (64, 16384, 260), (3, 16384, 260), (20, 16384, 260),
+         (2, 40, 8200), (20, 40, 8200), (3, 33, 7), (2, 5, 1)]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f16"])
