@@ -7,7 +7,7 @@ Six kinds of pass:
                `pre` the sums before the activation come too, as a backward pass wants them
   act_grad     dZ = dY * act'(Z) and the bias's gradient, the column sums of dZ
   linear_grad  the backward pass of a linear layer: dZ and the bias's gradient, then dX = dZ . W and dW = dZ^T . X in 8 bits (the
-               gradient in e5m2), every operand quantised within the call along its own reduction
+               gradient in e5m2), every operand quantised within the call along its own reduction; dX and dW in X's and W's type
   norm         layer norm, with the row's mean and 1 / deviation where a backward pass follows
   norm_grad    its backward pass: dX and the gradients of its weight and bias
 
@@ -179,7 +179,7 @@ def prepare(case, seed):
     z = torch.randn(M, N, generator=g, device="cuda").to(dtype)
     state = dict(case=case, x=x, w=w.to(dtype), z=z, dy=_gradients(g, M, N, dtype), dz=torch.empty_like(z))
     state["dbias"] = torch.empty(N, device="cuda")
-    state["dx"], state["dw"] = torch.empty_like(x), torch.empty(N, K, device="cuda")
+    state["dx"], state["dw"] = torch.empty_like(x), torch.empty_like(state["w"])
     state["workspace"] = _act_grad_workspace(M, N)
     state["dz_rows"], state["w_cols"] = _packed(M, N, E5M2), _packed(K, N, E4M3, 128)
     state["dz_cols"], state["x_cols"] = _packed(N, M, E5M2), _packed(K, M, E4M3)
@@ -336,7 +336,7 @@ def run(state):
     dx = torch.matmul(d, w.t()).to(state["x"].dtype)
     d = _dequantize(*_quantize(dz.t(), E5M2), M)
     x = _dequantize(*_quantize(state["x"].t(), E4M3), M)
-    return dx, torch.matmul(d, x.t()), dbias
+    return dx, torch.matmul(d, x.t()).to(state["w"].dtype), dbias
 
 
 # ---- what a pass cannot do without -----------------------------------------------------------------------------------------
@@ -365,7 +365,7 @@ def work(case):
         w = M * K * s + N * K * (1 + 1 / 128 ** 2) + N * _SIZE[case["bias"]] + M * N * _SIZE[case["y"]] * outs
         return {"bytes": w, "flops": 2 * M * N * K}
     # dY, Z, X and W read, dX, dW and the bias's gradient written
-    return {"bytes": s * (2 * M * N + 2 * M * K + N * K) + 4 * N * K + 4 * N, "flops": 4 * M * N * K}
+    return {"bytes": s * (2 * M * N + 2 * M * K + 2 * N * K) + 4 * N, "flops": 4 * M * N * K}
 
 
 # ---- from the definition, in 64 bits ---------------------------------------------------------------------------------------
