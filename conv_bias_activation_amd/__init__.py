@@ -10,6 +10,9 @@ this package raises ImportError — there is no fallback path.
     conv2d_bias_act(x, w, bias, y, strides=(1, 1), pads=(0, 0, 0, 0), dilations=(1, 1), act="tanh")
     gemm_bias_act_2k(..., workspace=ws) / conv2d_bias_act_2k(..., workspace=ws)
     mxfp4_quantize(X, codes, scales); gemm_mxfp4_bias_act(A, a_scales, B, b_scales, bias, C, act="gelu")
+    fp8_quantize(X, codes, scales); gemm_fp8_bias_act(A, a_scales, B, b_scales, bias, C, act="gelu", Z=Z)
+    bias_act_grad(dY, Z, dZ, dbias, act="gelu", workspace=ws)
+    layer_norm(X, gamma, beta, Y, mean, rstd); layer_norm_grad(dY, X, gamma, mean, rstd, dX, dgamma, dbeta, workspace=ws)
 """
 from ._binding import (  # noqa: F401
     ACT_CODES,
@@ -42,6 +45,16 @@ from ._binding import (  # noqa: F401
     gemm_bias_act_workspace_size,
     gemm_mxfp4_bias_act,
     gemm_mxfp4_bias_add_act,
+    bias_act_grad,
+    bias_act_grad_workspace_size,
+    fp8_dequantize,
+    fp8_quantize,
+    fp8_shapes,
+    gemm_fp8_bias_act,
+    gemm_fp8_bias_add_act,
+    layer_norm,
+    layer_norm_grad,
+    layer_norm_grad_workspace_size,
     gemm_tile_config,
     conv_tile_config,
     lib,

@@ -10,7 +10,8 @@ from typing import Optional, Sequence
 _HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_HERE, "libbiasact.so")
 
-DTYPE_CODES = {"f32": 0, "f16": 1, "bf16": 2, "i8": 3, "i32": 4, "mxfp4": 5}
+DTYPE_CODES = {"f32": 0, "f16": 1, "bf16": 2, "i8": 3, "i32": 4, "mxfp4": 5, "f8e4m3": 6,
+               "f8e5m2": 7}
 ACT_CODES = {"none": 0, "relu": 1, "leaky_relu": 2, "tanh": 3, "gelu": 4, "sigmoid": 5}
 BA_OK, BA_ERR_INVALID, BA_ERR_UNSUPPORTED, BA_ERR_HIP = 0, 1, 2, 3
 
@@ -118,6 +119,27 @@ def _load():
     l.gemm_mxfp4_bias_act.restype = ctypes.c_int
     l.gemm_mxfp4_bias_add_act.argtypes = [vp] * 7 + [i64, i64, i64, u32, ctypes.c_int, ctypes.c_float, vp]
     l.gemm_mxfp4_bias_add_act.restype = ctypes.c_int
+    ci, cf = ctypes.c_int, ctypes.c_float
+    l.fp8_packed_size.argtypes = [i64, i64, ci, u64p, u64p]
+    l.fp8_packed_size.restype = ci
+    l.fp8_quantize.argtypes = [vp, vp, vp, i64, i64, ci, ci, u32, vp]
+    l.fp8_quantize.restype = ci
+    l.fp8_dequantize.argtypes = l.fp8_quantize.argtypes
+    l.fp8_dequantize.restype = ci
+    l.gemm_fp8_bias_act.argtypes = [vp, vp, ci, vp, vp, ci, vp, vp, vp, i64, i64, i64, u32, ci, cf, vp]
+    l.gemm_fp8_bias_act.restype = ci
+    l.gemm_fp8_bias_add_act.argtypes = [vp, vp, ci, vp, vp, ci, vp, vp, vp, vp, i64, i64, i64, u32, ci, cf, vp]
+    l.gemm_fp8_bias_add_act.restype = ci
+    l.bias_act_grad_workspace_size.argtypes = [i64, i64]
+    l.bias_act_grad_workspace_size.restype = ctypes.c_size_t
+    l.bias_act_grad.argtypes = [vp, vp, vp, vp, i64, i64, u32, ci, cf, vp, ctypes.c_size_t, vp]
+    l.bias_act_grad.restype = ci
+    l.layer_norm.argtypes = [vp] * 6 + [i64, i64, cf, u32, vp]
+    l.layer_norm.restype = ci
+    l.layer_norm_grad_workspace_size.argtypes = [i64, i64]
+    l.layer_norm_grad_workspace_size.restype = ctypes.c_size_t
+    l.layer_norm_grad.argtypes = [vp] * 8 + [i64, i64, u32, vp, ctypes.c_size_t, vp]
+    l.layer_norm_grad.restype = ci
     return l
 
 
@@ -125,7 +147,7 @@ lib = _load()
 
 
 def _load_native():
-    """The C++ way from torch tensors to the MXFP4 calls (native_call.cpp), or
+    """The C++ way from torch tensors to the MXFP4, 8-bit, layer norm and gradient calls (native_call.cpp), or
     None where torch or the module is missing, or where the module does not
     load (built for another torch or Python; a warning says why): the calls
     below then marshal through ctypes, to the same entry points."""
@@ -144,12 +166,15 @@ def _load_native():
         m = importlib.util.module_from_spec(importlib.util.spec_from_loader(loader.name, loader))
         loader.exec_module(m)
     except ImportError as e:
-        warnings.warn(f"{path} does not load ({e}); the MXFP4 calls go through ctypes, which costs them up to "
-                      "3 us of host time. Rebuild with `python conv_bias_activation_amd/build.py`.", RuntimeWarning,
+        warnings.warn(f"{path} does not load ({e}); the MXFP4, 8-bit and layer norm calls go through ctypes, "
+                      "which costs them up to 5 us of host time. Rebuild with `python conv_bias_activation_amd/build.py`.", RuntimeWarning,
                       stacklevel=2)
         return None
     m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         lib.mxfp4_quantize, lib.mxfp4_dequantize, lib.gemm_mxfp4_bias_act, lib.gemm_mxfp4_bias_add_act)))
+    m.bind_layer(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.fp8_quantize, lib.fp8_dequantize, lib.gemm_fp8_bias_act, lib.gemm_fp8_bias_add_act, lib.bias_act_grad,
+        lib.layer_norm, lib.layer_norm_grad)))
     return m
 
 
@@ -654,6 +679,258 @@ def gemm_mxfp4_bias_add_act(A, a_scales, B, b_scales, bias, R, C, act="none", al
     if rc:
         _check(rc, "gemm_mxfp4_bias_add_act")
     return C
+
+
+# -- 8-bit floating point -------------------------------------------------------
+
+def _here(t, name):
+    """_dev, and on the current device: its stream takes the call."""
+    p = _dev(t, name)
+    if t is not None and t.device.index != _torch().cuda.current_device():
+        raise ValueError(f"{name} must be on the current device")
+    return p
+
+
+def fp8_shapes(rows: int, K: int, block_rows: int = 1):
+    """Shapes of the codes (float8_e4m3fn or float8_e5m2) and scales (uint8)
+    of `rows` rows of K values with a scale for each 128 of a row, or
+    (block_rows 128) for each 128 x 128."""
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    return (rows, (K + 127) // 128 * 128), (-(-rows // block_rows), (K + 511) // 512 * 4)
+
+
+_F8 = None          # torch dtype -> element type name, built on first use
+
+
+def _f8_packed(codes, scales, name):
+    """(rows, blocks of k, block_rows, element type name) of a packed operand."""
+    global _F8
+    if _F8 is None:
+        torch = _torch()
+        _F8 = {torch.float8_e4m3fn: "f8e4m3", torch.float8_e5m2: "f8e5m2"}
+    f8 = _F8.get(codes.dtype)
+    if f8 is None or scales.dtype is not _torch().uint8:
+        raise ValueError(f"{name}: codes must be float8_e4m3fn or float8_e5m2 and scales uint8, got "
+                         f"{codes.dtype} and {scales.dtype}")
+    if codes.dim() == 2 and scales.dim() == 2 and codes.shape[1] % 128 == 0:
+        rows, kb = codes.shape[0], codes.shape[1] // 128
+        for block_rows in (1, 128):
+            if tuple(scales.shape) == (-(-rows // block_rows), (kb + 3) // 4 * 4):
+                return rows, kb, block_rows, f8
+    raise ValueError(f"{name}: codes must be [rows, 128 b] and scales [rows or ceil(rows / 128), 4 ceil(b / 4)], got "
+                     f"{tuple(codes.shape)} and {tuple(scales.shape)}")
+
+
+def _f8_quant_args(X, codes, scales, axis, name):
+    if X.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if axis not in (0, 1):
+        raise ValueError("axis must be 0 or 1")
+    rows, K = X.shape if axis == 1 else (X.shape[1], X.shape[0])
+    r, kb, block_rows, f8 = _f8_packed(codes, scales, "fp8")
+    if (r, kb) != (rows, (K + 127) // 128):
+        raise ValueError(f"codes and scales must be {fp8_shapes(rows, K)} or {fp8_shapes(rows, K, 128)}, got "
+                         f"{tuple(codes.shape)} and {tuple(scales.shape)}")
+    return rows, K, int(axis), block_rows, dtypes_code(_tname(X), f8, None, "f32")
+
+
+def fp8_quantize(X, codes, scales, axis: int = 1, stream=None):
+    """Quantises X to the codes' type with blocks of 128 along `axis`: the rows
+    of X[rows, K] (axis 1) or the columns of X[K, rows] (axis 0).  codes and
+    scales (fp8_shapes(rows, K[, 128]): the scales' shape says whether a block
+    spans one row or 128) are written and returned."""
+    if stream is None and _native is not None:
+        rc = _native.f8_quantize(X, codes, scales, axis)
+        if rc is True:
+            return codes, scales
+        if rc:                                   # the library's status; False: not called
+            _check(rc, "fp8_quantize")
+    rows, K, axis, block_rows, dt = _f8_quant_args(X, codes, scales, axis, "X")
+    rc = lib.fp8_quantize(_here(X, "X"), _here(codes, "codes"), _here(scales, "scales"), rows, K, axis, block_rows,
+                          dt, _stream(stream))
+    _check(rc, "fp8_quantize")
+    return codes, scales
+
+
+def fp8_dequantize(codes, scales, Y, axis: int = 1, stream=None):
+    """The values that codes and scales stand for, in Y's type and in Y's
+    layout ([rows, K] with axis 1, [K, rows] with axis 0)."""
+    if stream is None and _native is not None:
+        rc = _native.f8_dequantize(Y, codes, scales, axis)
+        if rc is True:
+            return Y
+        if rc:
+            _check(rc, "fp8_dequantize")
+    rows, K, axis, block_rows, dt = _f8_quant_args(Y, codes, scales, axis, "Y")
+    rc = lib.fp8_dequantize(_here(codes, "codes"), _here(scales, "scales"), _here(Y, "Y"), rows, K, axis, block_rows,
+                            dt, _stream(stream))
+    _check(rc, "fp8_dequantize")
+    return Y
+
+
+def _gemm_f8_args(A, a_scales, B, b_scales, bias, C, Z):
+    M, ka, block_a, fa = _f8_packed(A, a_scales, "A")
+    N, kb, block_b, fb = _f8_packed(B, b_scales, "B")
+    if ka != kb or tuple(C.shape) != (M, N):
+        raise ValueError(f"shape mismatch: A{tuple(A.shape)} B{tuple(B.shape)} C{tuple(C.shape)}")
+    if bias is not None and bias.numel() != N:
+        raise ValueError(f"bias must have N = {N} elements")
+    if Z is not None and (Z.shape != C.shape or Z.dtype != C.dtype):
+        raise ValueError(f"Z must match C: {tuple(C.shape)} {C.dtype}, got {tuple(Z.shape)} {Z.dtype}")
+    dt = dtypes_code(fa, fb, None if bias is None else _tname(bias), _tname(C))
+    return (block_a, block_b), (M, N, 128 * ka, dt)
+
+
+def gemm_fp8_bias_act(A, a_scales, B, b_scales, bias, C, act="none", alpha: float = 0.0, Z=None, stream=None):
+    """C = act(A @ B.T + bias), A and B in 8-bit floating point (codes and
+    scales of their M and N rows).  Z, like C, takes the sums before the
+    activation, which bias_act_grad wants."""
+    if stream is None and _native is not None:
+        rc = _native.f8_gemm(A, a_scales, B, b_scales, bias, None, Z, C, act, alpha)
+        if rc is True:
+            return C
+        if rc:
+            _check(rc, "gemm_fp8_bias_act")
+    (block_a, block_b), sizes = _gemm_f8_args(A, a_scales, B, b_scales, bias, C, Z)
+    rc = lib.gemm_fp8_bias_act(_here(A, "A"), _here(a_scales, "a_scales"), block_a, _here(B, "B"),
+                               _here(b_scales, "b_scales"), block_b, _here(bias, "bias"), _here(Z, "Z"), _here(C, "C"),
+                               *sizes, _act(act), float(alpha), _stream(stream))
+    _check(rc, "gemm_fp8_bias_act")
+    return C
+
+
+def gemm_fp8_bias_add_act(A, a_scales, B, b_scales, bias, R, C, act="none", alpha: float = 0.0, Z=None,
+                          stream=None):
+    """C = act(A @ B.T + bias + R); R like C (may be C itself)."""
+    if stream is None and _native is not None and R is not None:
+        rc = _native.f8_gemm(A, a_scales, B, b_scales, bias, R, Z, C, act, alpha)
+        if rc is True:
+            return C
+        if rc:
+            _check(rc, "gemm_fp8_bias_add_act")
+    (block_a, block_b), sizes = _gemm_f8_args(A, a_scales, B, b_scales, bias, C, Z)
+    _residual(R, C)
+    rc = lib.gemm_fp8_bias_add_act(_here(A, "A"), _here(a_scales, "a_scales"), block_a, _here(B, "B"),
+                                   _here(b_scales, "b_scales"), block_b, _here(bias, "bias"), _here(R, "R"),
+                                   _here(Z, "Z"), _here(C, "C"), *sizes, _act(act), float(alpha), _stream(stream))
+    _check(rc, "gemm_fp8_bias_add_act")
+    return C
+
+
+# -- layer norm and gradients ------------------------------------------------------
+
+def _vector(t, n, name, dtype=None):
+    if t is None:
+        return None
+    if t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    return _here(t, name)
+
+
+def _like(t, other, name, of, same_type=True):
+    if tuple(t.shape) != tuple(other.shape) or (same_type and t.dtype != other.dtype):
+        raise ValueError(f"{name} must match {of}: {tuple(other.shape)} {other.dtype}, got {tuple(t.shape)} {t.dtype}")
+    return _here(t, name)
+
+
+def _workspace_of(workspace, needed: int, name: str):
+    if workspace is None:
+        if needed:
+            raise ValueError(f"workspace (device buffer of {name}_workspace_size bytes) is required")
+        return None, 0
+    return _here(workspace, "workspace"), workspace.numel() * workspace.element_size()
+
+
+def bias_act_grad_workspace_size(M: int, N: int) -> int:
+    return int(lib.bias_act_grad_workspace_size(M, N))
+
+
+def bias_act_grad(dY, Z, dZ, dbias=None, act="none", alpha: float = 0.0, workspace=None, stream=None):
+    """dZ = dY * act'(Z) and dbias = the column sums of dZ: the gradient of
+    act(z), z = A @ B + bias (+ R), for every product here.  Z may be None for
+    act "none", dZ or dbias where it is not wanted; dZ may be dY or Z.  dbias
+    needs workspace (bias_act_grad_workspace_size bytes).  Returns (dZ, dbias)."""
+    if stream is None and _native is not None:
+        rc = _native.act_grad(dY, Z, dZ, dbias, act, alpha, workspace)
+        if rc is True:
+            return dZ, dbias
+        if rc:
+            _check(rc, "bias_act_grad")
+    if dY.dim() != 2:
+        raise ValueError("dY must be 2-D")
+    M, N = dY.shape
+    dt = dtypes_code(_tname(dY), "f32", None if dbias is None else _tname(dbias), "f32")
+    ws, nbytes = _workspace_of(workspace, M and N and dbias is not None, "bias_act_grad")
+    rc = lib.bias_act_grad(_here(dY, "dY"), None if Z is None else _like(Z, dY, "Z", "dY"),
+                           None if dZ is None else _like(dZ, dY, "dZ", "dY"), _vector(dbias, N, "dbias"), M, N, dt,
+                           _act(act), float(alpha), ws, nbytes, _stream(stream))
+    _check(rc, "bias_act_grad")
+    return dZ, dbias
+
+
+def _norm_dtypes(X, vectors, Y):
+    w = None
+    for name, t in vectors:
+        if t is not None:
+            if w is not None and t.dtype != w.dtype:
+                raise ValueError(f"{name} must be {w.dtype} like the other weights, got {t.dtype}")
+            w = t
+    return dtypes_code(_tname(X), "f32" if w is None else _tname(w), "f32", _tname(Y))
+
+
+def layer_norm(X, gamma, beta, Y, mean=None, rstd=None, eps: float = 1e-5, stream=None):
+    """Y = (X - mean) * rstd * gamma + beta over the rows of X, rstd =
+    1 / sqrt(variance + eps); gamma and beta may be None.  mean and rstd (fp32, one
+    a row) are written where given, as layer_norm_grad wants them.  Returns Y."""
+    if stream is None and _native is not None:
+        rc = _native.norm(X, gamma, beta, Y, mean, rstd, eps)
+        if rc is True:
+            return Y
+        if rc:
+            _check(rc, "layer_norm")
+    if X.dim() != 2:
+        raise ValueError("X must be 2-D")
+    rows, N = X.shape
+    f32 = _torch().float32
+    dt = _norm_dtypes(X, (("gamma", gamma), ("beta", beta)), Y)
+    rc = lib.layer_norm(_here(X, "X"), _vector(gamma, N, "gamma"), _vector(beta, N, "beta"),
+                        _like(Y, X, "Y", "X", same_type=False), _vector(mean, rows, "mean", f32),
+                        _vector(rstd, rows, "rstd", f32), rows, N, float(eps), dt, _stream(stream))
+    _check(rc, "layer_norm")
+    return Y
+
+
+def layer_norm_grad_workspace_size(rows: int, N: int) -> int:
+    return int(lib.layer_norm_grad_workspace_size(rows, N))
+
+
+def layer_norm_grad(dY, X, gamma, mean, rstd, dX, dgamma=None, dbeta=None, workspace=None, stream=None):
+    """The gradient of layer_norm: dX, and where given dgamma and dbeta, from
+    dY and the forward pass's X, gamma, mean and rstd.  dgamma and dbeta (gamma's
+    type) need workspace (layer_norm_grad_workspace_size bytes).  Returns (dX, dgamma, dbeta)."""
+    if stream is None and _native is not None:
+        rc = _native.norm_grad(dY, X, gamma, mean, rstd, dX, dgamma, dbeta, workspace)
+        if rc is True:
+            return dX, dgamma, dbeta
+        if rc:
+            _check(rc, "layer_norm_grad")
+    if X.dim() != 2:
+        raise ValueError("X must be 2-D")
+    rows, N = X.shape
+    f32 = _torch().float32
+    if mean is None or rstd is None:
+        raise ValueError("mean and rstd of the forward pass are required")
+    dt = _norm_dtypes(X, (("gamma", gamma), ("dgamma", dgamma), ("dbeta", dbeta)), dY)
+    ws, nbytes = _workspace_of(workspace, rows and N and (dgamma is not None or dbeta is not None), "layer_norm_grad")
+    rc = lib.layer_norm_grad(_like(dY, X, "dY", "X", same_type=False), _here(X, "X"), _vector(gamma, N, "gamma"),
+                             _vector(mean, rows, "mean", f32), _vector(rstd, rows, "rstd", f32),
+                             _like(dX, X, "dX", "X"), _vector(dgamma, N, "dgamma"), _vector(dbeta, N, "dbeta"),
+                             rows, N, dt, ws, nbytes, _stream(stream))
+    _check(rc, "layer_norm_grad")
+    return dX, dgamma, dbeta
 
 
 # -- tile configs ------------------------------------------------------------

@@ -35,8 +35,10 @@ _TYPES = ("f32", "f16", "bf16")
 HIP_SOURCES = ["api.hip", "act_cast.hip", "dispatch.hip"] + [
     f"{op}_{ti}_{to}.hip" for op in ("gemm", "conv") for ti in _TYPES for to in _TYPES] + [
     f"gemm_i8_{to}.hip" for to in ("f32", "f16", "bf16", "i32")] + [
-    "mx_quant.hip"] + [f"gemm_mx_{ta}.hip" for ta in ("mxfp4", "f16", "bf16")]
-CPP_SOURCES = ["plan.cpp", "plan_mx.cpp"]
+    "mx_quant.hip"] + [f"gemm_mx_{ta}.hip" for ta in ("mxfp4", "f16", "bf16")] + [
+    "api_f8.hip", "f8_quant.hip", "api_norm.hip", "act_grad.hip"] + [
+    f"{op}_{t}.hip" for op in ("gemm_f8", "layer_norm") for t in _TYPES]
+CPP_SOURCES = ["plan.cpp", "plan_mx.cpp", "plan_f8.cpp", "plan_norm.cpp"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-I", INCLUDE, "-I", CSRC, "-Wall",
           "-Wno-unused-command-line-argument"]
@@ -112,7 +114,7 @@ def build(jobs: int | None = None, verbose: bool = False) -> str:
     else:
         if os.path.exists(NATIVE):                   # of an earlier build, perhaps for another library
             os.remove(NATIVE)
-        print(f"{os.path.basename(NATIVE)} is not built, the MXFP4 calls will go through ctypes: {no_native}", flush=True)
+        print(f"{os.path.basename(NATIVE)} is not built, the MXFP4, 8-bit and layer norm calls will go through ctypes: {no_native}", flush=True)
     tmp = LIB + ".tmp"
     _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *sorted(objs)])
     os.replace(tmp, LIB)

@@ -20,15 +20,11 @@ using namespace biasact;
 namespace biasact {
 thread_local hipError_t t_launch_error = hipSuccess;
 thread_local char t_launch_desc[kLaunchDescBytes] = "none";
-}
-
-namespace {
 
 // the HIP error behind the most recent BA_ERR_HIP on this thread
-thread_local hipError_t t_last_hip = hipSuccess;
+static thread_local hipError_t t_last_hip = hipSuccess;
 
-// Status of the launches queued since the last call (launch_kernel records
-// the first refusal).
+// launch_kernel records the first refusal
 int launch_status() {
   const hipError_t e = t_launch_error;
   t_launch_error = hipSuccess;
@@ -36,6 +32,9 @@ int launch_status() {
   t_last_hip = e;
   return kErrHip;
 }
+}
+
+namespace {
 
 int out_bytes(int dt) { return (dt == DT_F32 || dt == DT_I32) ? 4 : 2; }
 

@@ -1,0 +1,342 @@
+// gemm_f8_tile.hpp — tiled fused product of two 8-bit operands on gfx950:
+//   C[M,N] = act(A . B^T + bias (+ R)), both operands as rows of k (f8_args.hpp)
+//
+// Workgroup: WM x WN waves (m x n) of SJ x SI accumulator blocks of 32x32
+// each: an output tile of 32 SJ WM (m) x 32 SI WN (n).  A k-step is one block of
+// 128 values: a whole cache line per row and one scale.
+//
+// Codes reach LDS without passing through registers, 16 bytes a lane, two
+// stages deep; chunk c of row r lies at slot c ^ (r / 2 % 8).  The matrix
+// instruction v_mfma_scale_f32_32x32x64 applies both scales itself; within a
+// block all k share them, so any assignment of the block's k to instructions and
+// lanes will do that is the same for both operands: instruction ks takes the
+// chunks 4 ks .. 4 ks + 3, two of them from each half of the wave.
+// A word of four scale bytes serves four steps; the words travel through
+// registers into LDS, one word a row, and the instruction's operand selector
+// picks the step's byte.
+//
+// Registers: 128 sums a lane at 4 x 2 blocks, and the operands of two quarters of
+// a step: a quarter multiplies one k-half of half the wave's rows of A by all its
+// rows of B while the next quarter's operands are read.
+#pragma once
+
+#include "f8_args.hpp"
+#include "f8_launch.hpp"
+#include "launch_kernel.hpp"
+#include "tile_epilogue.hpp"
+#include "tile_map.hpp"
+
+namespace biasact {
+
+namespace f8 {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+// the instruction's code of an operand's format
+constexpr int fmt(int dt) { return dt == DT_E4M3 ? 0 : 1; }
+
+struct Frag { u32x4 lo, hi; };                         // 32 codes of a lane
+
+__device__ __forceinline__ i32x8 regs(const Frag& f) {
+  typedef uint32_t u32x8 __attribute__((ext_vector_type(8)));
+  return __builtin_bit_cast(i32x8, (u32x8)__builtin_shufflevector(f.lo, f.hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// acc += b . a^T over 64 k, scale byte KS of each word
+template <int FB, int FA, int KS>
+__device__ __forceinline__ f32x16 mfma32(const Frag& b, const Frag& a, f32x16 acc, uint32_t sb, uint32_t sa) {
+  constexpr int fb = fmt(FB), fa = fmt(FA);
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(regs(b), regs(a), acc, fb, fa, KS, (int)sb, KS, (int)sa);
+}
+
+// acc += b . a^T over 128 k, scale byte 0 of each word
+template <int FB, int FA>
+__device__ __forceinline__ f32x4 mfma16(const Frag& b, const Frag& a, f32x4 acc, uint32_t sb, uint32_t sa) {
+  constexpr int fb = fmt(FB), fa = fmt(FA);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(regs(b), regs(a), acc, fb, fa, 0, (int)sb, 0, (int)sa);
+}
+
+// ---- products whose sums are to be fp32 throughout -----------------------------------
+// The 8-bit instructions above add eight neighbouring products in fixed point: what
+// lies 2^14 or more below the leading bit that the largest of the eight can have
+// is cut off (measured on single products: 2^2 beside 2^16 vanishes, 2^3 stays), which
+// leaves a result of many terms 5e-5 off (2-norm) without a bias.  A 16-bit output rounds
+// by 2e-4 or more; an fp32 output would show it, so there the codes are widened
+// to bf16 with their scale, which is exact within bf16's range, and bf16
+// instructions form the sums, at half the rate.
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// eight codes (two words) -> bf16 with their scale (exponent field of s)
+template <int F>
+__device__ __forceinline__ bf16x8 widen8(uint32_t lo, uint32_t hi, float s) {
+  u32x4 v;
+  if constexpr (F == DT_E4M3) {
+    v.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, false));
+    v.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, true));
+    v.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, false));
+    v.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, true));
+  } else {
+    v.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, s, false));
+    v.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, s, true));
+    v.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, s, false));
+    v.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, s, true));
+  }
+  return __builtin_bit_cast(bf16x8, v);
+}
+
+// codes 8 q .. 8 q + 7 of the 32
+template <int F>
+__device__ __forceinline__ bf16x8 widen_part(const Frag& f, int q, float s) {
+  const u32x4 h = q < 2 ? f.lo : f.hi;
+  return widen8<F>(h[2 * (q & 1)], h[2 * (q & 1) + 1], s);
+}
+
+// scale byte i of a word as cvt_scalef32 takes it
+__device__ __forceinline__ float scale_field(uint32_t word, int i) { return __uint_as_float(((word >> (8 * i)) & 255u) << 23); }
+
+// f(format of A, format of B) as integral constants: the kernels are made for each
+// pair, since one kernel with a loop for each has no registers left (it spilled 97)
+template <class F>
+inline void with_formats(int fa, int fb, F&& f) {
+  constexpr std::integral_constant<int, DT_E4M3> e4{};
+  constexpr std::integral_constant<int, DT_E5M2> e5{};
+  if (fa == DT_E4M3) {
+    if (fb == DT_E4M3) f(e4, e4);
+    else f(e4, e5);
+  } else {
+    if (fb == DT_E4M3) f(e5, e4);
+    else f(e5, e5);
+  }
+}
+
+template <int WM, int WN, int SJ, int SI>
+struct Tile {
+  static constexpr int THREADS = 64 * WM * WN, BM = 32 * SJ * WM, BN = 32 * SI * WN;
+  static constexpr int A_STAGE = BM * 128, B_STAGE = BN * 128, S_BUF = (BM + BN) * 4;
+  static constexpr int A_OFF = 0, B_OFF = 2 * A_STAGE, S_OFF = B_OFF + 2 * B_STAGE;
+  static constexpr int BIAS_OFF = S_OFF + 2 * S_BUF, LDS_BYTES = BIAS_OFF + BN * 4;
+  static constexpr int A_LOADS = BM * 128 / 16 / THREADS, B_LOADS = BN * 128 / 16 / THREADS;   // per wave and step
+  static constexpr int S_LOADS = (BM + BN) / THREADS;                                          // scale words per thread
+  static_assert(BN <= THREADS, "bias");
+  static_assert(SJ % 2 == 0, "halves of A's rows");
+  static_assert((BM + BN) % THREADS == 0 && BM % 64 == 0, "scale rows");
+  static_assert(A_LOADS % 2 == 0 && B_LOADS % 2 == 0, "pairs of loads share a swizzle");
+  static_assert(BM * BN * 2 <= BIAS_OFF && 32 * SJ * BN * 4 <= BIAS_OFF, "epilogue staging");
+  static_assert(LDS_BYTES <= 160 * 1024, "LDS");
+};
+
+constexpr int WAIT_LGKM0 = 0xC07F;
+constexpr int wait_vm(int n) { return 0x0F70 | (n & 0xF) | ((n >> 4) << 14); }
+
+}  // namespace f8
+
+template <int FA, int FB, int DTO, int WM, int WN, int SJ, int SI>
+__global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8GemmArgs a) {
+  using T = f8::Tile<WM, WN, SJ, SI>;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[T::LDS_BYTES];
+
+  uint32_t tm, tn;
+  map_tile(blockIdx.x, gridDim.x, a.tiles_m, a.tiles_n, tm, tn);
+  const uint32_t m0 = tm * T::BM, n0 = tn * T::BN;
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = w / WN, wn = w % WN;
+  const int half = lane >> 5, lrow = lane & 31;
+  const int steps = (int)a.KB;                // >= 1
+
+  f32x16 acc[SI][SJ];
+#pragma unroll
+  for (int si = 0; si < SI; ++si)
+#pragma unroll
+    for (int sj = 0; sj < SJ; ++sj)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[si][sj][r] = 0.0f;
+
+  // ---- direct loads: 8 rows of 128 bytes each ---------------------------------------
+  // Rows past the end read as zeros (or, where a huge offset wraps, as other
+  // rows); their sums are not stored.  The main loop has no branches: loads for
+  // which there is no step have a buffer of no bytes, i.e. fetch nothing.
+  // Lane l fills slot l % 8 of row l / 8 of its eight; the swizzle of the odd
+  // eights differs by 4, i.e. by 64 bytes of the row.
+  const uint32_t chunk = (lane & 7) ^ ((lane >> 4) & 3);
+  const uint32_t a_off = (m0 + T::A_LOADS * 8 * w + (lane >> 3)) * a.KB * 128u + chunk * 16u;
+  const uint32_t b_off = (n0 + T::B_LOADS * 8 * w + (lane >> 3)) * a.KB * 128u + chunk * 16u;
+  constexpr int LOADS = T::A_LOADS + T::B_LOADS;
+  // loads [from, to) of this wave's share of step s, into stage st
+  auto issue = [&](int s, int st, int from, int to) __attribute__((always_inline)) {
+    const bool more = s < steps;
+    const __amdgpu_buffer_rsrc_t ra = make_rsrc(a.A, more ? a.a_bytes : 0u);
+    const __amdgpu_buffer_rsrc_t rb = make_rsrc(a.B, more ? a.b_bytes : 0u);
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      if (i < from || i >= to) continue;
+      const int j = i < T::A_LOADS ? i : i - T::A_LOADS;
+      const uint32_t more_off = 8u * j * a.KB * 128u + s * 128u;
+      if (i < T::A_LOADS)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(smem + T::A_OFF + st * T::A_STAGE + (T::A_LOADS * w + j) * 1024), 16,
+                                                 (a_off ^ (64u * (j & 1))) + more_off, 0, 0, 0);
+      else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(smem + T::B_OFF + st * T::B_STAGE + (T::B_LOADS * w + j) * 1024), 16,
+                                                 (b_off ^ (64u * (j & 1))) + more_off, 0, 0, 0);
+    }
+  };
+
+  // ---- scales: thread t brings the words of rows t (and t + THREADS) of A's rows followed by B's
+  auto load_scales = [&](int W, uint32_t (&v)[T::S_LOADS]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < T::S_LOADS; ++i) {
+      const int row0 = i * T::THREADS + 64 * w;        // uniform; BM is a multiple of 64
+      const bool of_a = row0 < T::BM, any = W < (int)a.KW;
+      const __amdgpu_buffer_rsrc_t rs =
+          of_a ? make_rsrc(a.As, any ? a.as_bytes : 0u) : make_rsrc(a.Bs, any ? a.bs_bytes : 0u);
+      const uint32_t row = of_a ? (m0 + row0 + lane) >> a.ash : (n0 + (row0 - T::BM) + lane) >> a.bsh;
+      v[i] = ld_b32(rs, (row * a.KW + W) * 4u);
+    }
+  };
+  auto put_scales = [&](int W, const uint32_t (&v)[T::S_LOADS]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < T::S_LOADS; ++i)
+      *reinterpret_cast<uint32_t*>(smem + T::S_OFF + (W & 1) * T::S_BUF + (i * T::THREADS + 64 * w + lane) * 4) = v[i];
+  };
+
+  // ---- LDS fragment addresses: row lrow, chunk 4 ks + 2 half + (0, 1) ------------------
+  const uint32_t fr = lrow * 128 + (((2 * half) ^ ((lrow >> 1) & 7)) * 16);
+  const uint32_t a_rd = T::A_OFF + wm * 32 * SJ * 128 + fr, b_rd = T::B_OFF + wn * 32 * SI * 128 + fr;
+
+  // ---- main loop ---------------------------------------------------------------------
+  // Step s, quarters (k-half, half of A's rows) (0,0) (0,1) (1,0) (1,1): each reads
+  // the next quarter's operands, then multiplies.  The one barrier comes before the
+  // last quarter, after this wave's loads of step s + 1 have landed and its reads
+  // of step s are done: from there on stage s + 1 may be read and stage s
+  // overwritten.
+  // this tile's bias (zeros past N or without one): its bits now, fp32 into LDS later
+  const __amdgpu_buffer_rsrc_t rbias = make_rsrc(a.bias, a.bias_dt >= 0 ? a.bias_bytes : 0u);
+  const uint32_t bias_n = n0 + threadIdx.x;
+  const bool bias_ok = threadIdx.x < T::BN && bias_n < a.N;
+  uint32_t bias;
+  if (a.bias_dt == DT_F32) bias = ld_b32(rbias, bias_ok ? bias_n * 4u : kOOB);
+  else bias = ld_b16(rbias, bias_ok ? bias_n * 2u : kOOB);
+  uint32_t snext[T::S_LOADS];
+  load_scales(0, snext);
+  issue(0, 0, 0, LOADS);
+  put_scales(0, snext);
+  if (threadIdx.x < T::BN)
+    *reinterpret_cast<float*>(smem + T::BIAS_OFF + threadIdx.x * 4) =
+        a.bias_dt == DT_F16 ? widen<DT_F16>(bias) : a.bias_dt == DT_BF16 ? widen<DT_BF16>(bias) : widen<DT_F32>(bias);
+  const uint32_t sc_rd = T::S_OFF + lrow * 4;
+  constexpr bool WIDE = DTO == DT_F32;
+  constexpr int HJ = SJ / 2;                           // blocks of A's rows a quarter
+  f8::Frag fa[2][HJ], fb[2][SI];                       // by half of A's rows; by k-half
+  uint32_t wa[2][SJ], wb[2][SI];                       // scale words, by parity of the word
+  auto frag = [&](uint32_t at) __attribute__((always_inline)) {
+    return f8::Frag{*reinterpret_cast<const u32x4*>(smem + at), *reinterpret_cast<const u32x4*>(smem + (at ^ 16u))};
+  };
+  auto read_a = [&](int ks, int p, int st) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < HJ; ++j) fa[p][j] = frag((a_rd ^ (64u * ks)) + st * T::A_STAGE + (p * HJ + j) * 4096);
+  };
+  auto read_b = [&](int ks, int st) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < SI; ++i) fb[ks][i] = frag((b_rd ^ (64u * ks)) + st * T::B_STAGE + i * 4096);
+  };
+  auto read_scales = [&](int W, int odd) __attribute__((always_inline)) {
+    const uint8_t* sp = smem + sc_rd + (W & 1) * T::S_BUF;
+#pragma unroll
+    for (int i = 0; i < SI; ++i) wb[odd][i] = *reinterpret_cast<const uint32_t*>(sp + (T::BM + wn * 32 * SI + i * 32) * 4);
+#pragma unroll
+    for (int j = 0; j < SJ; ++j) wa[odd][j] = *reinterpret_cast<const uint32_t*>(sp + (wm * 32 * SJ + j * 32) * 4);
+  };
+  auto join = [&]() __attribute__((always_inline)) {
+    __builtin_amdgcn_s_waitcnt(f8::wait_vm(0));
+    __builtin_amdgcn_s_waitcnt(f8::WAIT_LGKM0);
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  join();
+  read_scales(0, 0);
+  read_b(0, 0);
+  read_a(0, 0, 0);
+  issue(1, 1, 0, LOADS / 2);
+  auto multiply = [&](int ks, int p, auto sel_c, int odd) __attribute__((always_inline)) {
+    constexpr int SEL = decltype(sel_c)::value;
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (WIDE) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        bf16x8 b[SI], x[HJ];
+#pragma unroll
+        for (int si = 0; si < SI; ++si) b[si] = f8::widen_part<FB>(fb[ks][si], q, f8::scale_field(wb[odd][si], SEL));
+#pragma unroll
+        for (int j = 0; j < HJ; ++j) x[j] = f8::widen_part<FA>(fa[p][j], q, f8::scale_field(wa[odd][p * HJ + j], SEL));
+#pragma unroll
+        for (int si = 0; si < SI; ++si)
+#pragma unroll
+          for (int j = 0; j < HJ; ++j)
+            acc[si][p * HJ + j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[si], x[j], acc[si][p * HJ + j], 0, 0, 0);
+      }
+    } else {
+#pragma unroll
+      for (int si = 0; si < SI; ++si)
+#pragma unroll
+        for (int j = 0; j < HJ; ++j) {
+          const int sj = p * HJ + j;
+          acc[si][sj] = f8::mfma32<FB, FA, SEL>(fb[ks][si], fa[p][j], acc[si][sj], wb[odd][si], wa[odd][sj]);
+        }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // step s (of scale word W = s / 4, parity odd), byte SEL = s % 4, stage s % 2
+  auto step = [&](int s, auto sel_c, int odd) __attribute__((always_inline)) {
+    constexpr int SEL = decltype(sel_c)::value;
+    constexpr int st = SEL & 1;
+    read_a(0, 1, st);
+    if constexpr (SEL == 0) load_scales((s >> 2) + 1, snext);
+    issue(s + 1, st ^ 1, LOADS / 2, LOADS);
+    multiply(0, 0, sel_c, odd);
+    read_b(1, st);
+    read_a(1, 0, st);
+    multiply(0, 1, sel_c, odd);
+    read_a(1, 1, st);
+    if constexpr (SEL == 2) put_scales((s >> 2) + 1, snext);
+    multiply(1, 0, sel_c, odd);
+    join();
+    read_b(0, st ^ 1);                               // (past the last step: whatever is there, unused)
+    read_a(0, 0, st ^ 1);
+    if constexpr (SEL == 3) read_scales((s >> 2) + 1, odd ^ 1);
+    issue(s + 2, st, 0, LOADS / 2);
+    multiply(1, 1, sel_c, odd);
+  };
+  constexpr std::integral_constant<int, 0> b0{};
+  constexpr std::integral_constant<int, 1> b1{};
+  constexpr std::integral_constant<int, 2> b2{};
+  constexpr std::integral_constant<int, 3> b3{};
+  for (int s = 0; s < steps; s += 8) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int t = s + 4 * h;
+      if (t < steps) step(t, b0, h);
+      if (t + 1 < steps) step(t + 1, b1, h);
+      if (t + 2 < steps) step(t + 2, b2, h);
+      if (t + 3 < steps) step(t + 3, b3, h);
+    }
+  }
+  // no direct load (of zeros) may still be writing LDS when the epilogue reuses it
+  __builtin_amdgcn_s_waitcnt(f8::wait_vm(0));
+  tile_epilogue<DTO, WM, WN, SJ, SI>(a, smem, T::BIAS_OFF, m0, n0, acc);
+}
+
+template <int DTO, int WM, int WN, int SJ, int SI>
+inline void launch_f8_tile(F8GemmArgs a, hipStream_t s) {
+  using T = f8::Tile<WM, WN, SJ, SI>;
+  a.tiles_n = (a.N + T::BN - 1) / T::BN;
+  a.tiles_m = (a.M + T::BM - 1) / T::BM;
+  note_launch("gemm fp8 tile, %d m x %d n", T::BM, T::BN);
+  f8::with_formats(a.fa, a.fb, [&](auto fa_c, auto fb_c) {
+    launch_kernel(f8_tile_kernel<decltype(fa_c)::value, decltype(fb_c)::value, DTO, WM, WN, SJ, SI>, dim3(a.tiles_m * a.tiles_n),
+                  dim3(T::THREADS), s, a);
+  });
+}
+
+}  // namespace biasact

@@ -17,6 +17,9 @@ namespace biasact {
 // clears it before each entry point's launches).
 extern thread_local hipError_t t_launch_error;
 
+// Status of the launches queued since the last call (kOk or kErrHip; api.hip).
+int launch_status();
+
 // Description of the main kernel the calling thread queued last (reported by
 // biasact_last_tile_config).
 constexpr int kLaunchDescBytes = 96;

@@ -1,0 +1,45 @@
+// norm_plan.hpp — how the rows of the gradient kernels are divided, which the
+// workspaces' sizes follow (host and kernels' launches; no device code).
+#pragma once
+
+#include <stdint.h>
+
+namespace biasact {
+
+// Rows longer than this are read again for each step of a layer norm; up to it
+// a row stays in its threads' registers.
+constexpr uint32_t kNormLong = 65536u, kNormGradLong = 32768u;
+
+// Threads that share a row of N values in layer_norm_grad (16 to 1024), and the
+// rows that a workgroup of 256 or more then takes at once.
+inline uint32_t norm_grad_threads(uint32_t N) {
+  return N <= 128u ? 16u : N <= 1024u ? 64u : N <= 8192u ? 256u : 1024u;
+}
+inline uint32_t norm_grad_rows_at_once(uint32_t N) {
+  const uint32_t t = norm_grad_threads(N);
+  return t >= 256u ? 1u : 256u / t;
+}
+
+// Workgroups that each keep the column sums of their share of the rows.
+inline uint32_t norm_grad_parts(uint32_t rows, uint32_t N) {
+  if (N > kNormGradLong) return rows < 64u ? rows : 64u;
+  const uint32_t once = norm_grad_rows_at_once(N), groups = (rows + once - 1) / once;
+  const uint32_t most = norm_grad_threads(N) >= 1024u ? 256u : 1024u;
+  return groups < most ? groups : most;
+}
+
+// Lanes (as a power of two) that share a row of N values in bias_act_grad, eight
+// columns a lane, and the row splits for M rows.
+inline uint32_t act_grad_lane_bits(uint32_t N) {
+  uint32_t b = 0;
+  while (b < 6u && (8u << b) < N) ++b;
+  return b;
+}
+inline uint32_t act_grad_parts(uint32_t M, uint32_t N) {
+  const uint32_t b = act_grad_lane_bits(N), tiles = (N + (8u << b) - 1) / (8u << b);
+  const uint32_t once = 256u >> b;                     // rows that a workgroup takes at once
+  const uint32_t groups = (M + once - 1) / once, want = (2048u + tiles - 1) / tiles;
+  return groups < want ? groups : want;
+}
+
+}  // namespace biasact

@@ -78,6 +78,51 @@ int plan_mx_quant(const void* X, const void* codes, const void* scales, int64_t 
 int plan_mx_gemm(const void* A, const void* As, const void* B, const void* Bs, const void* bias, const void* R,
                  const void* C, int64_t M, int64_t N, int64_t K, uint32_t dtypes, int act, MxGemmPlan* p);
 
+// 8-bit floating-point operators (plan_f8.cpp); KB = ceil(K / 128) blocks and
+// KW = ceil(K / 512) words of scales a row.
+struct F8QuantPlan {
+  int dt, f8;
+  uint32_t rows, K, KB, KW, sh;    // sh: 0 for a scale a row, 7 for 128 rows
+  bool empty;                      // nothing to launch
+};
+
+struct F8GemmPlan {
+  int fa, fb, dto, bias_dt;        // bias_dt = -1 without bias
+  uint32_t M, N, KB, KW, ash, bsh;
+  uint32_t a_bytes, as_bytes, b_bytes, bs_bytes, bias_bytes, c_bytes;
+  bool empty;                      // M == 0 or N == 0: nothing to launch
+};
+
+int f8_sizes(int64_t rows, int64_t K, int block_rows, int64_t* codes_bytes, int64_t* scales_bytes);
+int plan_f8_quant(const void* X, const void* codes, const void* scales, int64_t rows, int64_t K, int k_axis,
+                  int block_rows, uint32_t dtypes, F8QuantPlan* p);
+int plan_f8_gemm(const void* A, const void* As, int a_block_rows, const void* B, const void* Bs, int b_block_rows,
+                 const void* bias, const void* R, const void* Z, const void* C, int64_t M, int64_t N, int64_t K,
+                 uint32_t dtypes, int act, F8GemmPlan* p);
+
+// Layer norm and the gradients (plan_norm.cpp).
+struct NormPlan {
+  int dtx, dtw, dty;               // X (and dX), gamma and beta (and their gradients), Y (or dY)
+  uint32_t rows, N;
+  bool empty;                      // rows == 0 or N == 0
+};
+
+struct ActGradPlan {
+  int dt, dtb;                     // dY, Z and dZ; dbias
+  uint32_t M, N;
+  bool empty;
+};
+
+int plan_layer_norm(const void* X, const void* gamma, const void* beta, const void* Y, const void* mean,
+                    const void* rstd, int64_t rows, int64_t N, float eps, uint32_t dtypes, NormPlan* p);
+int plan_layer_norm_grad(const void* dY, const void* X, const void* gamma, const void* mean, const void* rstd,
+                         const void* dX, const void* dgamma, const void* dbeta, int64_t rows, int64_t N,
+                         uint32_t dtypes, const void* workspace, size_t workspace_bytes, NormPlan* p);
+int plan_bias_act_grad(const void* dY, const void* Z, const void* dZ, const void* dbias, int64_t M, int64_t N,
+                       uint32_t dtypes, int act, const void* workspace, size_t workspace_bytes, ActGradPlan* p);
+size_t layer_norm_grad_workspace(int64_t rows, int64_t N);
+size_t bias_act_grad_workspace(int64_t M, int64_t N);
+
 // Output size of conv2d with zero padding (floor rounding); kErrInvalid for
 // bad strides / pads / dilations or an empty output.
 int conv_out_dims(int64_t H, int64_t W, int64_t kh, int64_t kw, const int32_t* strides,

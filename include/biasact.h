@@ -54,13 +54,15 @@
 extern "C" {
 #endif
 
-/* element type codes (storage size: 4, 2, 2, 1, 4 bytes) */
+/* element type codes (storage size: 4, 2, 2, 1, 4 bytes, half a byte, 1, 1) */
 #define BA_F32 0u
 #define BA_F16 1u
 #define BA_BF16 2u
 #define BA_I8 3u            /* two's complement int8: GEMM operands only */
 #define BA_I32 4u           /* two's complement int32: bias / output of int8 GEMMs */
 #define BA_MXFP4 5u         /* 4-bit floating point in scaled blocks (below): gemm_mxfp4_* operands only */
+#define BA_F8E4M3 6u        /* 8-bit floating point in scaled blocks (below): fp8_* and gemm_fp8_* operands only, */
+#define BA_F8E5M2 7u        /* 4 exponent and 3 mantissa bits (OCP e4m3), or 5 and 2 */
 
 /* dtypes argument: one 8-bit code per operand.
  *   a   : A (GEMM) or x (conv)
@@ -251,6 +253,116 @@ int gemm_mxfp4_bias_add_act(const void* A, const void* a_scales, const void* B,
                             const void* b_scales, const void* bias, const void* R, void* C,
                             int64_t M, int64_t N, int64_t K, uint32_t dtypes, int act, float alpha,
                             hipStream_t stream);
+
+/* 8-bit floating point in blocks of 128 values with a shared scale, for
+ * inference and training.  A value is a code (OCP e4m3: the largest is 448,
+ * there is no infinity; or e5m2: 57344) times its block's scale 2^(b - 127), b
+ * one byte; b = 255 is NaN.  Blocks run along the reduction index k, 128 values
+ * of one row (block_rows 1) or of 128 rows (block_rows 128; the last block of
+ * rows may be short).  An operand of `rows` rows of K values is two packed arrays:
+ *   codes  [rows, 128 * ceil(K / 128)] bytes,
+ *   scales [ceil(rows / block_rows), 4 * ceil(K / 512)] bytes, byte j for the k
+ *          from 128 j on,
+ * i.e. each row of codes is padded to whole blocks (zero codes) and each row of
+ * scales to whole words, whose bytes past the last block are never used
+ * (fp8_quantize writes zeros).  codes must be 16-byte and scales 4-byte aligned
+ * (BA_ERR_INVALID otherwise).
+ *
+ * fp8_packed_size: bytes of the two arrays (host pointers). */
+int fp8_packed_size(int64_t rows, int64_t K, int block_rows, size_t* codes_bytes, size_t* scales_bytes);
+
+/* X -> codes, scales.  dtypes = BA_DTYPES(x, f8, 0, 0): X is fp32, fp16 or bf16,
+ * packed [rows, K] with k_axis = 1, or [K, rows] with k_axis = 0 (each column
+ * becomes one row of codes); f8 is BA_F8E4M3 or BA_F8E5M2.  Per block: the scale
+ * is the smallest power of two 2^e for which max|x| / 2^e is at most the format's
+ * largest value, e clamped to [-127, 127]; scale byte e + 127; each code is x / 2^e
+ * rounded to nearest, ties to even.  A block of zeros takes scale byte 0.
+ * Infinities and NaN do not count for the scale: NaN becomes the format's NaN
+ * (0x7f with x's sign), infinity NaN in e4m3 and infinity in e5m2.  rows, K >= 0
+ * (either 0: nothing to do). */
+int fp8_quantize(const void* X, void* codes, void* scales, int64_t rows, int64_t K, int k_axis,
+                 int block_rows, uint32_t dtypes, hipStream_t stream);
+
+/* codes, scales -> Y, laid out and typed like X above: each value's code times
+ * its scale, rounded to nearest even where Y's type cannot hold it. */
+int fp8_dequantize(const void* codes, const void* scales, void* Y, int64_t rows, int64_t K, int k_axis,
+                   int block_rows, uint32_t dtypes, hipStream_t stream);
+
+/* C[M,N] = act(A[M,K] . B[N,K]^T + bias[N])  and  act(A . B^T + bias + R), both
+ * operands in 8 bits as above (dtypes' a and b: BA_F8E4M3 or BA_F8E5M2, in any
+ * combination), each with its own block_rows.  bias and out: fp32, fp16 or bf16
+ * each; R has C's type and shape and may be C itself.  Z, where it is not NULL,
+ * takes A . B^T + bias (+ R) in C's type and shape, which a backward pass needs
+ * (bias_act_grad); it must not overlap C or R (BA_ERR_INVALID where it is one of
+ * them).  Bias, residual and activation run in fp32 with one rounding each to C and to Z.
+ * With an fp32 C the products are exact and their sum is fp32, over the operands' values
+ * as bf16 holds them (exactly, where they lie below 2^128 and are no multiples of less than 2^-133).
+ * With a 16-bit C the 8-bit matrix instructions form the sum, twice as fast: they
+ * add the products of eight neighbouring k in fixed point, each cut off at 2^-13 of the
+ * power of two that the largest product's exponents give, and the rest in fp32; on a sum of
+ * many terms that is some 5e-5 of its size (2-norm), below half a step of the output.
+ * The order of a sum depends on the sizes and types alone, so equal calls give equal bits.  A value that is not finite affects its row (of
+ * A) or column (of B) only.  M, N, K >= 0 (M or N == 0: nothing to do; K == 0:
+ * C = act(bias (+ R))).  The gradients of act(X W^T + bias) are two more such
+ * products: dX = dZ . W, over operands dZ [M,N] and W^T [K,N], and dW = dZ^T . X,
+ * over dZ^T [N,M] and X^T [K,M], which fp8_quantize with k_axis = 0 makes from
+ * dZ, W and X as they lie.  Checks, limits and return codes otherwise as
+ * gemm_bias_act / gemm_bias_add_act; the forced tile configuration does not
+ * apply. */
+int gemm_fp8_bias_act(const void* A, const void* a_scales, int a_block_rows, const void* B,
+                      const void* b_scales, int b_block_rows, const void* bias, void* Z, void* C,
+                      int64_t M, int64_t N, int64_t K, uint32_t dtypes, int act, float alpha,
+                      hipStream_t stream);
+int gemm_fp8_bias_add_act(const void* A, const void* a_scales, int a_block_rows, const void* B,
+                          const void* b_scales, int b_block_rows, const void* bias, const void* R,
+                          void* Z, void* C, int64_t M, int64_t N, int64_t K, uint32_t dtypes, int act,
+                          float alpha, hipStream_t stream);
+
+/* Gradient of the epilogue of every product above, C = act(z), z = A . B + bias
+ * (+ R):  dZ = dY * act'(Z)  and  dbias[n] = sum over m of dZ[m, n].
+ * dtypes = BA_DTYPES(y, 0, bias, 0): dY, Z and dZ [M,N] of one type, dbias [N] of
+ * another, each fp32, fp16 or bf16.  Z holds the values before the activation;
+ * it may be NULL for BA_ACT_NONE, which does not read it.  dZ may be NULL (only the
+ * sums are wanted), and may be dY or Z itself, but not overlap them otherwise;
+ * dbias may be NULL; not both (BA_ERR_INVALID).  ReLU passes dY on where z > 0,
+ * LeakyReLU where z >= 0 and alpha * dY elsewhere.  The slope and the product run
+ * in fp32, the sums in fp32 over the products before they are rounded to dZ, in an
+ * order that depends on the sizes alone.  dbias needs `workspace`, a caller-owned,
+ * 16-byte aligned device buffer of at least bias_act_grad_workspace_size(M, N)
+ * bytes that no other work in flight uses (BA_ERR_INVALID without it).  M, N >= 0
+ * (N == 0: nothing to do; M == 0: dbias = 0). */
+size_t bias_act_grad_workspace_size(int64_t M, int64_t N);
+int bias_act_grad(const void* dY, const void* Z, void* dZ, void* dbias, int64_t M, int64_t N,
+                  uint32_t dtypes, int act, float alpha, void* workspace, size_t workspace_bytes,
+                  hipStream_t stream);
+
+/* Layer norm over the rows of X[rows, N], and its gradient.
+ *   Y = (X - mean) * rstd * gamma + beta,  rstd = 1 / sqrt(variance + eps)
+ * with each row's mean and (biased) variance over its N values.
+ * dtypes = BA_DTYPES(x, w, 0, y): X, gamma and beta (and dgamma and dbeta), and Y
+ * (and dY); each fp32, fp16 or bf16; dX has X's type.  gamma or beta may be NULL
+ * (ones, zeros).  mean and rstd, fp32 [rows], are written where they are not NULL
+ * (both or neither, BA_ERR_INVALID otherwise).  Statistics and all arithmetic are
+ * fp32, with one rounding to Y; a row's sum and sum of squares have to stay within
+ * fp32's range.  eps >= 0, finite; with eps = 0 a row of equal values gives NaN.  A value
+ * that is not finite affects its own row only.  Y may be X itself where their types
+ * are equal, but must not overlap it otherwise.  rows, N >= 0 (either 0: nothing to do). */
+int layer_norm(const void* X, const void* gamma, const void* beta, void* Y, float* mean, float* rstd,
+               int64_t rows, int64_t N, float eps, uint32_t dtypes, hipStream_t stream);
+
+/* With g = dY * gamma and xh = (X - mean) * rstd:
+ *   dX = rstd * (g - sum(g) / N - xh * sum(g * xh) / N)   (sums over the row),
+ *   dgamma = sum over rows of dY * xh,  dbeta = sum over rows of dY.
+ * mean and rstd are those of the forward pass.  dgamma, dbeta or both may be NULL;
+ * either needs `workspace`, a caller-owned, 16-byte aligned device buffer of at
+ * least layer_norm_grad_workspace_size(rows, N) bytes that no other work in flight
+ * uses (BA_ERR_INVALID without it).  dX may be X or dY itself where the types are equal
+ * and N is at most 32768, but must not overlap them otherwise.  Sums are fp32, in an order that
+ * depends on the sizes alone.  N == 0: nothing to do; rows == 0: dgamma = dbeta = 0. */
+size_t layer_norm_grad_workspace_size(int64_t rows, int64_t N);
+int layer_norm_grad(const void* dY, const void* X, const void* gamma, const float* mean,
+                    const float* rstd, void* dX, void* dgamma, void* dbeta, int64_t rows, int64_t N,
+                    uint32_t dtypes, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* Fused or two-kernel path, chosen per problem.  The pages decide at run
  * time whether to fuse: ops-nn (mlqm.cn/news/1824, sections
