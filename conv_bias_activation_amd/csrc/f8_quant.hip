@@ -18,6 +18,7 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef short s16x2 __attribute__((ext_vector_type(2)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
 // Eight consecutive values as they are stored (16 or 32 bytes).
 template <int DT> struct Raw8 { uint32_t w[2 * Elem<DT>::bytes]; };
@@ -59,23 +60,46 @@ __device__ __forceinline__ uint32_t mag_bits(const Raw8<DT>& v, int e) {
   else return (v.w[e >> 1] >> (16 * (e & 1))) & 0x7fffu;
 }
 
-template <int DT>
-__device__ __forceinline__ uint32_t max_bits(const Raw8<DT>& v) {
-  uint32_t m = 0;
+template <int DT, int NR>
+__device__ __forceinline__ uint32_t max_bits(const Raw8<DT> (&v)[NR]) {
+  if constexpr (Elem<DT>::bytes == 4) {
+    uint32_t m = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) m = max(m, mag_bits<DT>(v, e));
-  return m;
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = max(m, mag_bits<DT>(v[i], e));
+    return m;
+  } else {                                             // two at a time
+    u16x2 m = {0, 0};
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v[i].w[e] & 0x7fff7fffu));
+    return max((uint32_t)m.x, (uint32_t)m.y);
+  }
 }
 
 // The same over the finite values.
-template <int DT>
-__device__ __forceinline__ uint32_t max_finite_bits(const Raw8<DT>& v) {
+template <int DT, int NR>
+__device__ __forceinline__ uint32_t max_finite_bits(const Raw8<DT> (&v)[NR]) {
   uint32_t m = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t b = mag_bits<DT>(v, e);
-    m = max(m, b < kInfBits<DT> ? b : 0u);
-  }
+  for (int i = 0; i < NR; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t b = mag_bits<DT>(v[i], e);
+      m = max(m, b < kInfBits<DT> ? b : 0u);
+    }
+  return m;
+}
+
+// Bits of the largest finite magnitude, and whether any lane of the wave holds a
+// value that is not finite (rare: only then are the values looked at one by one).
+template <int DT, int NR>
+__device__ __forceinline__ uint32_t top_bits(const Raw8<DT> (&v)[NR], bool& odd) {
+  uint32_t m = max_bits<DT>(v);
+  odd = __any(m >= kInfBits<DT>);
+  if (__builtin_expect(odd, 0)) m = max_finite_bits<DT>(v);
   return m;
 }
 
@@ -191,15 +215,13 @@ __global__ __launch_bounds__(256) void f8_quantize_rows_kernel(F8QuantArgs a) {
   const uint32_t row = fdiv(wid, a.div), word = wid - row * a.KW;
   const uint32_t k0 = word * 512u + lane * 8u;
   const uint8_t* src = static_cast<const uint8_t*>(a.X) + (size_t)row * a.K * Elem<DT>::bytes;
-  Raw8<DT> v;
-  if (k0 + 8u <= a.K) v = load8<DT>(src + (size_t)k0 * Elem<DT>::bytes);
-  else v = load8_ragged<DT>(src, k0, a.K);
-  uint32_t m = max16(max_bits<DT>(v));
-  const bool odd = __any(m >= kInfBits<DT>);
-  if (odd) m = max16(max_finite_bits<DT>(v));
-  const uint32_t byte = scale_byte<DT, F8>(m);
-  u32x2 c = encode8<DT, F8>(v, byte);
-  if (odd) c = patch_nonfinite<DT, F8>(v, c);
+  Raw8<DT> v[1];
+  if (k0 + 8u <= a.K) v[0] = load8<DT>(src + (size_t)k0 * Elem<DT>::bytes);
+  else v[0] = load8_ragged<DT>(src, k0, a.K);
+  bool odd;
+  const uint32_t byte = scale_byte<DT, F8>(max16(top_bits<DT>(v, odd)));
+  u32x2 c = encode8<DT, F8>(v[0], byte);
+  if (__builtin_expect(odd, 0)) c = patch_nonfinite<DT, F8>(v[0], c);
   if (k0 < a.KB * 128u)
     *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(a.codes) + (size_t)row * a.KB * 128u + k0) = c;
   const uint32_t s = (uint32_t)__builtin_amdgcn_readlane((int)byte, 0) | (uint32_t)__builtin_amdgcn_readlane((int)byte, 16) << 8 |
@@ -215,16 +237,15 @@ __global__ __launch_bounds__(256) void f8_quantize_blocks_kernel(F8QuantArgs a) 
   const uint32_t rb = fdiv(blockIdx.x, a.div), kb = blockIdx.x - rb * a.KB;
   const uint32_t k0 = kb * 128u + (threadIdx.x & 15u) * 8u, row0 = rb * 128u + (threadIdx.x >> 4);
   Raw8<DT> v[8];
-  uint32_t m = 0;
 #pragma unroll
   for (uint32_t i = 0; i < 8; ++i) {
     const uint32_t row = row0 + 16u * i;
     const uint8_t* src = static_cast<const uint8_t*>(a.X) + (size_t)row * a.K * Elem<DT>::bytes;
     if (row < a.rows && k0 + 8u <= a.K) v[i] = load8<DT>(src + (size_t)k0 * Elem<DT>::bytes);
     else v[i] = load8_ragged<DT>(src, k0, row < a.rows ? a.K : 0u);
-    m = max(m, max_finite_bits<DT>(v[i]));
   }
-  m = max16(m);
+  bool odd;
+  uint32_t m = max16(top_bits<DT>(v, odd));
   m = max(m, (uint32_t)__shfl_xor((int)m, 16));
   m = max(m, (uint32_t)__shfl_xor((int)m, 32));
   if ((threadIdx.x & 63u) == 0) part[threadIdx.x >> 6] = m;
@@ -234,76 +255,75 @@ __global__ __launch_bounds__(256) void f8_quantize_blocks_kernel(F8QuantArgs a) 
 #pragma unroll
   for (uint32_t i = 0; i < 8; ++i) {
     const uint32_t row = row0 + 16u * i;
-    if (row < a.rows)
-      *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(a.codes) + (size_t)row * a.KB * 128u + k0) =
-          patch_nonfinite<DT, F8>(v[i], encode8<DT, F8>(v[i], byte));
+    u32x2 c = encode8<DT, F8>(v[i], byte);
+    if (__builtin_expect(odd, 0)) c = patch_nonfinite<DT, F8>(v[i], c);
+    if (row < a.rows) *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(a.codes) + (size_t)row * a.KB * 128u + k0) = c;
   }
   // the last block also writes the word's rest
   const uint32_t end = kb + 1 == a.KB ? a.KW * 4u : kb + 1;
   if (threadIdx.x < end - kb) static_cast<uint8_t*>(a.scales)[(size_t)rb * a.KW * 4u + kb + threadIdx.x] = (uint8_t)(threadIdx.x ? 0u : byte);
 }
 
-// Two neighbouring values of a row; `two`: both are there.
+// Two neighbouring values of a row as they are stored, one word or two; `two`:
+// both are there, else the first alone where `one`.
+template <int DT> struct Pair { uint32_t w[Elem<DT>::bytes / 2]; };
 template <int DT>
-__device__ __forceinline__ void load_pair(const uint8_t* p, bool one, bool two, uint32_t& x, uint32_t& y) {
-  x = y = 0;
-  if constexpr (Elem<DT>::bytes == 4) {
-    if (two) {
-      u32x2 v;
-      __builtin_memcpy(&v, p, 8);
-      x = v.x, y = v.y;
-    } else if (one) {
-      x = *reinterpret_cast<const uint32_t*>(p);
-    }
-  } else {
-    if (two) {
-      uint32_t v;
-      __builtin_memcpy(&v, p, 4);
-      x = v & 0xffffu, y = v >> 16;
-    } else if (one) {
-      x = *reinterpret_cast<const uint16_t*>(p);
-    }
+__device__ __forceinline__ Pair<DT> load_pair(const uint8_t* p, bool one, bool two) {
+  Pair<DT> v;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(v) / 4; ++i) v.w[i] = 0;
+  if (two) {
+    __builtin_memcpy(&v, p, sizeof(v));
+  } else if (one) {
+    if constexpr (Elem<DT>::bytes == 4) v.w[0] = *reinterpret_cast<const uint32_t*>(p);
+    else v.w[0] = *reinterpret_cast<const uint16_t*>(p);
   }
+  return v;
 }
 
 // ---- X[K, rows]: blocks down the columns ------------------------------------------
-// A workgroup takes 128 k of 128 columns: wave w the k from 16 w on, a lane two
-// columns, so that a wave reads whole lines of X.  The columns' largest values
-// (or, with a scale for 128 x 128, the tile's) meet in LDS.  Codes leave through
-// LDS too, a column's 16-byte chunk w at slot w ^ (column / 2 % 8), so that
-// eight lanes store a column's whole cache line.
+// A workgroup takes two blocks of 128 k of 128 columns: wave w the k from 32 w on, a
+// lane two columns, so that a wave reads whole lines of X.  The columns' largest
+// values (or, with a scale for 128 x 128, the tile's) meet in LDS.  Codes leave
+// through LDS too, a column's 16-byte chunk c at slot c ^ (column / 2 % 16), so
+// that sixteen lanes store 256 bytes of a column.
 template <int DT, int F8>
 __global__ __launch_bounds__(512) void f8_quantize_cols_kernel(F8QuantArgs a) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[128 * 128];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[128 * 256];
   __shared__ uint32_t most[8][128];
   const uint32_t lane = threadIdx.x & 63u, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t kb = fdiv(blockIdx.x, a.div), n0 = (blockIdx.x - kb * a.div.div) * 128u;
-  const uint32_t n = n0 + 2u * lane, k0 = kb * 128u + 16u * w;
-  Raw8<DT> v[2][2];
+  const uint32_t kb = 2u * fdiv(blockIdx.x, a.div), n0 = (blockIdx.x - (kb >> 1) * a.div.div) * 128u;
+  const uint32_t n = n0 + 2u * lane, k0 = kb * 128u + 32u * w;
+  Pair<DT> x[32];
 #pragma unroll
-  for (int i = 0; i < 2 * Elem<DT>::bytes; ++i) v[0][0].w[i] = v[0][1].w[i] = v[1][0].w[i] = v[1][1].w[i] = 0;
-#pragma unroll
-  for (uint32_t j = 0; j < 16; ++j) {
+  for (uint32_t j = 0; j < 32; ++j) {
     const bool row = k0 + j < a.K;
-    uint32_t x, y;
-    load_pair<DT>(static_cast<const uint8_t*>(a.X) + ((size_t)(k0 + j) * a.rows + n) * Elem<DT>::bytes, row && n < a.rows,
-                  row && n + 1 < a.rows, x, y);
+    x[j] = load_pair<DT>(static_cast<const uint8_t*>(a.X) + ((size_t)(k0 + j) * a.rows + n) * Elem<DT>::bytes, row && n < a.rows,
+                         row && n + 1 < a.rows);
+  }
+  Raw8<DT> v[2][4];
+#pragma unroll
+  for (uint32_t j = 0; j < 32; j += 2) {
     if constexpr (Elem<DT>::bytes == 4) {
-      v[0][j >> 3].w[j & 7] = x;
-      v[1][j >> 3].w[j & 7] = y;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        v[c][j >> 3].w[j & 7] = x[j].w[c];
+        v[c][j >> 3].w[(j & 7) + 1] = x[j + 1].w[c];
+      }
     } else {
-      v[0][j >> 3].w[(j & 7) >> 1] |= x << (16 * (j & 1));
-      v[1][j >> 3].w[(j & 7) >> 1] |= y << (16 * (j & 1));
+      v[0][j >> 3].w[(j & 7) >> 1] = __builtin_amdgcn_perm(x[j + 1].w[0], x[j].w[0], 0x05040100u);
+      v[1][j >> 3].w[(j & 7) >> 1] = __builtin_amdgcn_perm(x[j + 1].w[0], x[j].w[0], 0x07060302u);
     }
   }
   uint32_t m[2];
+  bool odd[2];
 #pragma unroll
-  for (int c = 0; c < 2; ++c) m[c] = max(max_finite_bits<DT>(v[c][0]), max_finite_bits<DT>(v[c][1]));
+  for (int c = 0; c < 2; ++c) m[c] = top_bits<DT>(v[c], odd[c]);
   *reinterpret_cast<u32x2*>(&most[w][2 * lane]) = u32x2{m[0], m[1]};
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const u32x2 o = *reinterpret_cast<const u32x2*>(&most[i][2 * lane]);
+  for (int i = 0; i < 4; ++i) {
+    const u32x2 o = *reinterpret_cast<const u32x2*>(&most[(w & 4u) + i][2 * lane]);
     m[0] = max(m[0], o.x);
     m[1] = max(m[1], o.y);
   }
@@ -316,31 +336,38 @@ __global__ __launch_bounds__(512) void f8_quantize_cols_kernel(F8QuantArgs a) {
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     byte[c] = scale_byte<DT, F8>(m[c]);
-    const u32x2 lo = patch_nonfinite<DT, F8>(v[c][0], encode8<DT, F8>(v[c][0], byte[c]));
-    const u32x2 hi = patch_nonfinite<DT, F8>(v[c][1], encode8<DT, F8>(v[c][1], byte[c]));
-    *reinterpret_cast<u32x4*>(lds + (2 * lane + c) * 128u + ((w ^ (lane & 7u)) << 4)) = u32x4{lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+    for (uint32_t h = 0; h < 2; ++h) {
+      u32x2 lo = encode8<DT, F8>(v[c][2 * h], byte[c]), hi = encode8<DT, F8>(v[c][2 * h + 1], byte[c]);
+      if (__builtin_expect(odd[c], 0)) {
+        lo = patch_nonfinite<DT, F8>(v[c][2 * h], lo);
+        hi = patch_nonfinite<DT, F8>(v[c][2 * h + 1], hi);
+      }
+      *reinterpret_cast<u32x4*>(lds + (2 * lane + c) * 256u + (((2 * w + h) ^ (lane & 15u)) << 4)) = u32x4{lo.x, lo.y, hi.x, hi.y};
+    }
   }
-  // scale bytes; the last block of k also writes the word's rest
-  if (w == 0) {
+  // scale bytes: waves 0 and 4 for their blocks; the row's last block also writes its word's rest
+  const uint32_t b = kb + (w >> 2);
+  if ((w & 3u) == 0 && b < a.KB) {
     uint8_t* const s = static_cast<uint8_t*>(a.scales);
-    const uint32_t end = kb + 1 == a.KB ? a.KW * 4u : kb + 1;
+    const uint32_t end = b + 1 == a.KB ? a.KW * 4u : b + 1;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const bool in = a.sh ? lane == 0 && c == 0 : n + c < a.rows;
       uint8_t* const at = s + (size_t)(a.sh ? n0 >> 7 : n + c) * a.KW * 4u;
       if (in) {
-        at[kb] = (uint8_t)byte[c];
-        for (uint32_t b = kb + 1; b < end; ++b) at[b] = 0;
+        at[b] = (uint8_t)byte[c];
+        for (uint32_t e = b + 1; e < end; ++e) at[e] = 0;
       }
     }
   }
   __syncthreads();
 #pragma unroll
-  for (uint32_t i = 0; i < 2; ++i) {
-    const uint32_t c = 64u * i + (threadIdx.x >> 3), b = threadIdx.x & 7u;
-    if (n0 + c < a.rows)
-      *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(a.codes) + ((size_t)(n0 + c) * a.KB + kb) * 128u + b * 16u) =
-          *reinterpret_cast<const u32x4*>(lds + c * 128u + ((b ^ ((c >> 1) & 7u)) << 4));
+  for (uint32_t i = 0; i < 4; ++i) {
+    const uint32_t c = 32u * i + (threadIdx.x >> 4), q = threadIdx.x & 15u;
+    if (n0 + c < a.rows && kb + (q >> 3) < a.KB)
+      *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(a.codes) + ((size_t)(n0 + c) * a.KB + kb) * 128u + q * 16u) =
+          *reinterpret_cast<const u32x4*>(lds + c * 256u + ((q ^ ((c >> 1) & 15u)) << 4));
   }
 }
 
@@ -406,9 +433,8 @@ void launch(F8QuantArgs a, bool along_rows, bool back, hipStream_t s) {
   const uint32_t col_tiles = (a.rows + 127u) / 128u;
   if (!along_rows) {
     a.div = make_fastdiv(col_tiles);
-    const dim3 grid(col_tiles * a.KB);
-    if (back) launch_kernel(f8_dequantize_cols_kernel<DT, F8>, grid, dim3(512), s, a);
-    else launch_kernel(f8_quantize_cols_kernel<DT, F8>, grid, dim3(512), s, a);
+    if (back) launch_kernel(f8_dequantize_cols_kernel<DT, F8>, dim3(col_tiles * a.KB), dim3(512), s, a);
+    else launch_kernel(f8_quantize_cols_kernel<DT, F8>, dim3(col_tiles * ((a.KB + 1u) / 2u)), dim3(512), s, a);
   } else if (back) {
     a.div = make_fastdiv(a.KB * 16u);
     launch_kernel(f8_dequantize_rows_kernel<DT, F8>, dim3((a.rows * a.KB * 16u + 255u) / 256u), dim3(256), s, a);
