@@ -122,7 +122,7 @@ struct Tile {
   static_assert(SJ % 2 == 0, "halves of A's rows");
   static_assert((BM + BN) % THREADS == 0 && BM % 64 == 0, "scale rows");
   static_assert(A_LOADS % 2 == 0 && B_LOADS % 2 == 0, "pairs of loads share a swizzle");
-  static_assert(BM * BN * 2 <= BIAS_OFF && 32 * SJ * BN * 4 <= BIAS_OFF, "epilogue staging");
+  static_assert(SJ == 2 || SJ == 4, "epilogue passes");
   static_assert(LDS_BYTES <= 160 * 1024, "LDS");
 };
 
@@ -324,6 +324,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8GemmArgs a) 
   }
   // no direct load (of zeros) may still be writing LDS when the epilogue reuses it
   __builtin_amdgcn_s_waitcnt(f8::wait_vm(0));
+  static_assert(WM * WN * 32 * (32 * SI * Elem<DTO>::bytes + 16) <= T::BIAS_OFF, "epilogue staging");
   tile_epilogue<DTO, WM, WN, SJ, SI>(a, smem, T::BIAS_OFF, m0, n0, acc);
 }
 
