@@ -6,11 +6,11 @@
 // sums through LDS at the end, in wave order, so every result has one fixed
 // order of additions.
 //
-// k advances by blocks of 128, one v_mfma_scale_f32_16x16x128 each: lane (r, g)
-// takes the chunks of 16 codes g and 4 + g of row r (any assignment will do that
-// is the same for both operands, since a block has one scale), straight from
-// memory, so that a load covers 64 consecutive bytes of each of 16 rows and the
-// next one the rest of the same cache lines.
+// k advances by blocks of 128, one v_mfma_scale_f32_16x16x128 each.  Codes go to LDS
+// of the wave's own without passing through registers, eight lanes a row of 128
+// bytes, UN blocks under way (a register of each would allow two); chunk c of row
+// r lies at slot c ^ (r / 2 % 8).  Lane (r, g) takes the chunks g and 4 + g of row r:
+// any assignment will do that is the same for both operands, since a block has one scale.
 #pragma once
 
 #include "gemm_f8_tile.hpp"
@@ -24,8 +24,9 @@ __global__ __launch_bounds__(64 * NW) void f8_stream_kernel(F8GemmArgs a) {
   constexpr int TN = 16 * NB, TM = 16 * MB;
   // the waves' sums, [m][n] with n contiguous and 4 floats of padding a row,
   // which keeps the rows of one access on different banks
-  constexpr int LDR = TN + 4, SUMS = TM * LDR * 4;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[NW * SUMS];
+  constexpr int SUMS = TM * (TN + 4) * 4, STAGE = (TN + TM) * 128;
+  static_assert(NW * UN * STAGE <= 160 * 1024 && SUMS <= UN * STAGE, "LDS");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[NW * UN * STAGE];
 
   // neighbouring workgroups of an XCD share rows of B
   const uint32_t t = xcd_contiguous(blockIdx.x, gridDim.x);
@@ -44,57 +45,32 @@ __global__ __launch_bounds__(64 * NW) void f8_stream_kernel(F8GemmArgs a) {
   const uint32_t per = (a.KB + NW - 1) / NW;
   const uint32_t d0 = min(w * per, a.KB), d1 = min(d0 + per, a.KB);
 
-  f8::Frag bf[UN][NB], af[UN][MB];
+  // block d into stage u: lane l fills slot l % 8 of row l / 8 of each eight rows; the
+  // swizzle of the odd eights differs by 4, i.e. by 64 bytes of the row
+  uint8_t* const my = smem + w * (UN * STAGE);
+  const uint32_t chunk = ((lane & 7u) ^ ((lane >> 4) & 3u)) * 16u;
+  const uint32_t b_off = (n0 + (lane >> 3)) * a.KB * 128u + chunk, a_off = (m0 + (lane >> 3)) * a.KB * 128u + chunk;
   uint32_t bs[UN][NB], as[UN][MB];
   auto load = [&](int u, uint32_t d) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const uint32_t row = n0 + 16 * i + r, at = (row * a.KB + d) * 128u + g * 16u;
-      bf[u][i].lo = ld_b128(rb, at);
-      bf[u][i].hi = ld_b128(rb, at + 64u);
-      bs[u][i] = ld_b8(rbs, (row >> a.bsh) * a.KW * 4u + d);
-    }
+    for (int i = 0; i < 2 * NB; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(my + u * STAGE + i * 1024), 16,
+                                               (b_off ^ (64u * (i & 1))) + (8u * i * a.KB + d) * 128u, 0, 0, 0);
 #pragma unroll
-    for (int j = 0; j < MB; ++j) {
-      const uint32_t row = m0 + 16 * j + r, at = (row * a.KB + d) * 128u + g * 16u;
-      af[u][j].lo = ld_b128(ra, at);
-      af[u][j].hi = ld_b128(ra, at + 64u);
-      as[u][j] = ld_b8(ras, (row >> a.ash) * a.KW * 4u + d);
-    }
+    for (int j = 0; j < 2 * MB; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(my + u * STAGE + (2 * NB + j) * 1024), 16,
+                                               (a_off ^ (64u * (j & 1))) + (8u * j * a.KB + d) * 128u, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < NB; ++i) bs[u][i] = ld_b8(rbs, ((n0 + 16 * i + r) >> a.bsh) * a.KW * 4u + d);
+#pragma unroll
+    for (int j = 0; j < MB; ++j) as[u][j] = ld_b8(ras, ((m0 + 16 * j + r) >> a.ash) * a.KW * 4u + d);
   };
 #pragma unroll
   for (int u = 0; u < UN; ++u)
     if (d0 + u < d1) load(u, d0 + u);
 
-  // ---- bias and residual of this thread's outputs, under the main loop -----------------
-  // quad o (four consecutive n of one row) of the tile, o = threadIdx.x + 64 NW p
-  constexpr int QUADS = TM * TN / 4, P = (QUADS + 64 * NW - 1) / (64 * NW);
-  const __amdgpu_buffer_rsrc_t rc = make_rsrc(a.C, a.c_bytes), rz = make_rsrc(a.Z, a.Z ? a.c_bytes : 0u);
-  const __amdgpu_buffer_rsrc_t rr = make_rsrc(a.R, a.R ? a.c_bytes : 0u);
-  const bool vec = a.N % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.C) | reinterpret_cast<uintptr_t>(a.R) |
-                                     reinterpret_cast<uintptr_t>(a.Z)) & (4u * Elem<DTO>::bytes - 1u)) == 0;
-  float add[P][4];
-  uint32_t at[P];                                      // element offset of the quad, or kOOB
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    const uint32_t o = threadIdx.x + 64 * NW * p, ml = o / (TN / 4), nl = (o - ml * (TN / 4)) * 4;
-    const uint32_t m = m0 + ml, n = n0 + nl;
-    const bool in = o < (uint32_t)QUADS && m < a.M && n < a.N;
-    at[p] = in ? m * a.N + n : kOOB;
-    uint32_t idx[4] = {n, n + 1, n + 2, n + 3};
-    load_bias_vec<4>(a.bias, a.bias_bytes, a.bias_dt, idx, in ? a.N : 0u, add[p]);
-    if (a.R) {
-      float rv[4];
-      if (vec) {
-        load4<DTO>(rr, at[p], in, rv);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) rv[e] = load1<DTO>(rr, at[p] + e, in && n + e < a.N);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) add[p][e] += rv[e];
-    }
-  }
+  SumEpilogue<DTO, TM, TN, NW, 64 * NW> out;
+  out.load(a, m0, n0);                                 // under the main loop
 
   // ---- main loop -------------------------------------------------------------------
   f32x4 acc[NB][MB];
@@ -102,96 +78,120 @@ __global__ __launch_bounds__(64 * NW) void f8_stream_kernel(F8GemmArgs a) {
   for (int i = 0; i < NB; ++i)
 #pragma unroll
     for (int j = 0; j < MB; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const uint32_t get = r * 128u + ((g ^ ((r >> 1) & 7u)) << 4);   // chunk 4 + g: 64 bytes away
   for (uint32_t d = d0; d < d1; d += UN) {
 #pragma unroll
     for (int u = 0; u < UN; ++u)
       if (d + u < d1) {
+        // this block's loads have landed: those of later blocks may be under way
+        __builtin_amdgcn_sched_barrier(0);
+        if (d + u + UN - 1 < d1) __builtin_amdgcn_s_waitcnt(f8::wait_vm((UN - 1) * 3 * (NB + MB)));
+        else __builtin_amdgcn_s_waitcnt(f8::wait_vm(0));
+        __builtin_amdgcn_sched_barrier(0);
+        auto frag = [&](int at) __attribute__((always_inline)) {
+          const uint8_t* p = my + u * STAGE + at * 2048;
+          return f8::Frag{*reinterpret_cast<const u32x4*>(p + get), *reinterpret_cast<const u32x4*>(p + (get ^ 64u))};
+        };
+        f8::Frag af[MB];
 #pragma unroll
-        for (int i = 0; i < NB; ++i)
+        for (int j = 0; j < MB; ++j) af[j] = frag(NB + j);
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const f8::Frag bf = frag(i);
 #pragma unroll
           for (int j = 0; j < MB; ++j)
             if constexpr (DTO == DT_F32) {
 #pragma unroll
               for (int q = 0; q < 4; ++q)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                    f8::widen_part<FB>(bf[u][i], q, f8::scale_field(bs[u][i], 0)),
-                    f8::widen_part<FA>(af[u][j], q, f8::scale_field(as[u][j], 0)), acc[i][j], 0, 0, 0);
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f8::widen_part<FB>(bf, q, f8::scale_field(bs[u][i], 0)),
+                                                                    f8::widen_part<FA>(af[j], q, f8::scale_field(as[u][j], 0)),
+                                                                    acc[i][j], 0, 0, 0);
             } else {
-              acc[i][j] = f8::mfma16<FB, FA>(bf[u][i], af[u][j], acc[i][j], bs[u][i], as[u][j]);
+              acc[i][j] = f8::mfma16<FB, FA>(bf, af[j], acc[i][j], bs[u][i], as[u][j]);
             }
-        __builtin_amdgcn_sched_barrier(0);           // (loads ahead of the products would need registers of their own)
+        }
+        __builtin_amdgcn_sched_barrier(0);             // (the stage is read)
         if (d + u + UN < d1) load(u, d + u + UN);
       }
   }
 
   // ---- sums of the waves, epilogue ---------------------------------------------------
   // accumulator register e of lane (r, g): n = 16 i + 4 g + e, m = 16 j + r
-  auto sum = [&](uint32_t v, uint32_t ml, uint32_t nl) {
-    return reinterpret_cast<f32x4*>(smem + v * SUMS + (ml * LDR + nl) * 4u);
-  };
+  __syncthreads();                                     // the sums go over every wave's operands
 #pragma unroll
   for (int i = 0; i < NB; ++i)
 #pragma unroll
-    for (int j = 0; j < MB; ++j) *sum(w, 16 * j + r, 16 * i + 4 * g) = acc[i][j];
+    for (int j = 0; j < MB; ++j)
+      *reinterpret_cast<f32x4*>(smem + w * SUMS + ((16 * j + r) * (TN + 4) + 16 * i + 4 * g) * 4u) = acc[i][j];
   __syncthreads();
-  with_act(a.act, [&](auto act_c) __attribute__((always_inline)) {
-    constexpr int ACT = decltype(act_c)::value;
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      if (at[p] == kOOB) continue;
-      const uint32_t o = threadIdx.x + 64 * NW * p, ml = o / (TN / 4), nl = (o - ml * (TN / 4)) * 4;
-      f32x4 z = *sum(0, ml, nl);
-#pragma unroll
-      for (int v = 1; v < NW; ++v) z += *sum(v, ml, nl);
-      float y[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) z[e] += add[p][e];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] = mx::act<ACT, DTO>(z[e], a.alpha);
-      if (vec) {
-        if (a.Z) store4<DTO>(rz, at[p], true, z[0], z[1], z[2], z[3]);
-        store4<DTO>(rc, at[p], true, y[0], y[1], y[2], y[3]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (a.Z) store1<DTO>(rz, at[p] + e, n0 + nl + e < a.N, z[e]);
-          store1<DTO>(rc, at[p] + e, n0 + nl + e < a.N, y[e]);
-        }
-      }
-    }
-  });
+  out.store(a, smem, n0);
 }
 
-template <int DTO, int NB, int MB>
+template <int DTO, int NB, int MB, int UN>
 inline void launch_f8_stream(F8GemmArgs a, hipStream_t s) {
   constexpr int NW = 8;
   a.tiles_n = (a.N + 16 * NB - 1) / (16 * NB);
   a.tiles_m = (a.M + 16 * MB - 1) / (16 * MB);
   note_launch("gemm fp8 stream, %d n x %d m, k over %d waves", 16 * NB, 16 * MB, NW);
   f8::with_formats(a.fa, a.fb, [&](auto fa_c, auto fb_c) {
-    launch_kernel(f8_stream_kernel<decltype(fa_c)::value, decltype(fb_c)::value, DTO, NB, MB, NW, (NB * MB > 4 ? 1 : 2)>,
+    launch_kernel(f8_stream_kernel<decltype(fa_c)::value, decltype(fb_c)::value, DTO, NB, MB, NW, UN>,
                   dim3(a.tiles_m * a.tiles_n), dim3(64 * NW), s, a);
   });
 }
 
-inline uint64_t tiles_of(const F8GemmArgs& a, uint32_t bm, uint32_t bn) {
+// Choice of the kernel: the least estimated time.  Each kernel's workgroups take
+// the 256 CUs in rounds, and a round takes a part of its own and one for each
+// block of k.  The estimates, in 10 ns, fit these measurements (us, bf16 outputs):
+//   stream 16x16          8x4096x4096 4.2, 16x4096x16384 12.7, 64x4096x4096 10.9, 256x4096x1024 15.9
+//   stream 32 n x 16 m    32x4096x4096 5.3, 64x4096x4096 9.0
+//   wave   64 m x 32 n    64x4096x4096 7.1, 256x4096x4096 13.6, 64x1024x16384 16.4
+//   wave   64x64          64x4096x4096 9.2, 256x4096x4096 10.5, 512x4096x4096 20.0
+//   tile   128x128 deep   256x4096x4096 15.7, 512x4096x4096 16.4, 1024x4096x4096 21.0
+//   tile   128x128 twice  512x4096x4096 22.1, 1024x4096x4096 24.3, 2048x4096x4096 35
+//   tile   256x256        1024x4096x4096 38, 2048x4096x4096 41, 4096x4096x4096 57
+// (wave: each wave of four has a part of k; deep: one workgroup a CU with four
+// stages, for products of one round, whose step would else be a load's latency:
+// 4096x1024x32768 129, two stages 180; twice: two workgroups a CU.)
+inline uint64_t f8_tiles(const F8GemmArgs& a, uint32_t bm, uint32_t bn) {
   return (uint64_t)((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn);
 }
 
-// K = 0 (no blocks) runs the streaming kernel, whose waves then have nothing to add.
+enum { kF8Stream16, kF8Stream32, kF8Wave32, kF8Wave64, kF8TileDeep, kF8TileTwice, kF8TileLarge };
+
+inline int f8_choice(const F8GemmArgs& a, bool large) {
+  const uint64_t k = a.KB;
+  if (k == 0) return kF8Stream16;                      // whose waves then have nothing to add
+  const auto rounds = [](uint64_t tiles, uint64_t per) { return (tiles + per - 1) / per; };
+  const uint64_t t16 = f8_tiles(a, 16, 16), t32 = f8_tiles(a, 16, 32), w32 = f8_tiles(a, 64, 32), w64 = f8_tiles(a, 64, 64);
+  const uint64_t t128 = f8_tiles(a, 128, 128), t256 = f8_tiles(a, 256, 256);
+  const uint64_t rest128 = t128 % 512, rest256 = t256 % 256;
+  uint64_t cost[7];
+  cost[kF8Stream16] = 250 + 7 * k + (t16 > 256 ? (t16 - 256) * (k > 11 ? 7 * k : 80) / 256 : 0);
+  cost[kF8Stream32] = rounds(t32, 256) * (250 + 9 * k);
+  cost[kF8Wave32] = rounds(w32, 256) * (370 + 10 * k);
+  cost[kF8Wave64] = rounds(w64, 256) * (550 + 16 * k);
+  cost[kF8TileDeep] = rounds(t128, 256) * (500 + (t128 <= 128 ? 34 : 50) * k);
+  cost[kF8TileTwice] = t128 / 512 * (400 + 98 * k) + (rest128 == 0 ? 0 : rest128 <= 256 ? 400 + 62 * k : 400 + 98 * k);
+  cost[kF8TileLarge] = t256 / 256 * (1000 + 146 * k) + (rest256 == 0 ? 0 : rest256 <= 128 ? 900 + 92 * k : 1000 + 146 * k);
+  int best = 0;
+  for (int i = 1; i < (large ? 7 : 6); ++i)
+    if (cost[i] < cost[best]) best = i;
+  return best;
+}
+
+// (An fp32 output's widened operands leave no registers for the largest tile.)
 template <int DTO>
 inline void launch_gemm_f8(const F8GemmArgs& a, hipStream_t s) {
-  const uint64_t blocks = tiles_of(a, 64, 64);
-  if (a.KB > 0 && blocks > 256) {
-    const uint64_t t128 = tiles_of(a, 128, 128);
-    const uint64_t small = t128 <= 256 ? 15 : (t128 + 511) / 512 * 24, large = (tiles_of(a, 256, 256) + 255) / 256 * 40;
-    if constexpr (DTO != DT_F32)                       // (which has no registers for widened operands)
-      if (large < small) return launch_f8_tile<DTO, 2, 4, 4, 2>(a, s);
-    return launch_f8_tile<DTO, 2, 2, 2, 2>(a, s);
+  switch (f8_choice(a, DTO != DT_F32)) {
+    case kF8Stream16: return launch_f8_stream<DTO, 1, 1, 2>(a, s);
+    case kF8Stream32: return launch_f8_stream<DTO, 2, 1, 2>(a, s);
+    case kF8Wave32: return launch_f8_tile<DTO, 1, 1, 2, 1, 4, 2>(a, s);
+    case kF8Wave64: return launch_f8_tile<DTO, 1, 1, 2, 2, 4, 2>(a, s);
+    case kF8TileDeep: return launch_f8_tile<DTO, 2, 2, 2, 2, 1, 4>(a, s);
+    case kF8TileTwice: return launch_f8_tile<DTO, 2, 2, 2, 2, 1, 2>(a, s);
+    default:
+      if constexpr (DTO != DT_F32) launch_f8_tile<DTO, 2, 4, 4, 2, 1, 2>(a, s);
   }
-  if (a.M <= 16) return launch_f8_stream<DTO, 1, 1>(a, s);
-  if (a.M <= 32) return launch_f8_stream<DTO, 2, 2>(a, s);
-  launch_f8_stream<DTO, 4, 4>(a, s);
 }
 
 }  // namespace biasact

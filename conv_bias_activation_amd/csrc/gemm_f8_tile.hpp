@@ -1,9 +1,9 @@
 // gemm_f8_tile.hpp — tiled fused product of two 8-bit operands on gfx950:
 //   C[M,N] = act(A . B^T + bias (+ R)), both operands as rows of k (f8_args.hpp)
 //
-// Workgroup: WM x WN waves (m x n) of SJ x SI accumulator blocks of 32x32
-// each: an output tile of 32 SJ WM (m) x 32 SI WN (n).  A k-step is one block of
-// 128 values: a whole cache line per row and one scale.
+// Workgroup: KG groups, which divide k among them, of WM x WN waves (m x n) of
+// SJ x SI accumulator blocks of 32x32 each: an output tile of 32 SJ WM (m) x 32 SI WN
+// (n).  A k-step is one block of 128 values: a whole cache line per row and one scale.
 //
 // Codes reach LDS without passing through registers, 16 bytes a lane, two
 // stages deep; chunk c of row r lies at slot c ^ (r / 2 % 8).  The matrix
@@ -110,19 +110,25 @@ inline void with_formats(int fa, int fb, F&& f) {
   }
 }
 
-template <int WM, int WN, int SJ, int SI>
+template <int WM, int WN, int SJ, int SI, int KG, int ST>
 struct Tile {
-  static constexpr int THREADS = 64 * WM * WN, BM = 32 * SJ * WM, BN = 32 * SI * WN;
+  static constexpr int GW = WM * WN, THREADS = 64 * GW * KG, BM = 32 * SJ * WM, BN = 32 * SI * WN;
+  // of one group of waves: ST stages of codes, two words of scales a row
   static constexpr int A_STAGE = BM * 128, B_STAGE = BN * 128, S_BUF = (BM + BN) * 4;
-  static constexpr int A_OFF = 0, B_OFF = 2 * A_STAGE, S_OFF = B_OFF + 2 * B_STAGE;
-  static constexpr int BIAS_OFF = S_OFF + 2 * S_BUF, LDS_BYTES = BIAS_OFF + BN * 4;
-  static constexpr int A_LOADS = BM * 128 / 16 / THREADS, B_LOADS = BN * 128 / 16 / THREADS;   // per wave and step
-  static constexpr int S_LOADS = (BM + BN) / THREADS;                                          // scale words per thread
+  static constexpr int A_OFF = 0, B_OFF = ST * A_STAGE, S_OFF = B_OFF + ST * B_STAGE, GROUP = S_OFF + 2 * S_BUF;
+  static constexpr int BIAS_OFF = KG * GROUP, LDS_BYTES = BIAS_OFF + BN * 4;
+  // waves a SIMD that the registers are to allow: those of two workgroups a CU, where LDS does
+  static constexpr int WAVES = THREADS / 256 * (2 * LDS_BYTES <= 160 * 1024 ? 2 : 1);
+  static constexpr int A_LOADS = BM / 8 / GW, B_LOADS = BN / 8 / GW;   // per wave and step
+  static constexpr int S_LOADS = (BM + BN + 64 * GW - 1) / (64 * GW);  // scale words per thread
+  // the sums of a tile of one wave a group, rows 4 floats apart beyond their length
+  static constexpr int LDR = BN + 4, SUMS = BM * LDR * 4;
+  static_assert(ST == 2 || ST == 4, "a step's stage is known from its scale byte");
   static_assert(BN <= THREADS, "bias");
-  static_assert(SJ % 2 == 0, "halves of A's rows");
-  static_assert((BM + BN) % THREADS == 0 && BM % 64 == 0, "scale rows");
+  static_assert(SJ == 2 || SJ == 4, "halves of A's rows");
+  static_assert(BM % 64 == 0, "scale rows");
   static_assert(A_LOADS % 2 == 0 && B_LOADS % 2 == 0, "pairs of loads share a swizzle");
-  static_assert(SJ == 2 || SJ == 4, "epilogue passes");
+  static_assert(KG == 1 || (GW == 1 && KG * SUMS <= BIAS_OFF), "joining the groups");
   static_assert(LDS_BYTES <= 160 * 1024, "LDS");
 };
 
@@ -131,19 +137,24 @@ constexpr int wait_vm(int n) { return 0x0F70 | (n & 0xF) | ((n >> 4) << 14); }
 
 }  // namespace f8
 
-template <int FA, int FB, int DTO, int WM, int WN, int SJ, int SI>
-__global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8GemmArgs a) {
-  using T = f8::Tile<WM, WN, SJ, SI>;
+template <int FA, int FB, int DTO, int WM, int WN, int SJ, int SI, int KG, int ST>
+__global__ __launch_bounds__(64 * WM * WN * KG, (f8::Tile<WM, WN, SJ, SI, KG, ST>::WAVES)) void f8_tile_kernel(F8GemmArgs a) {
+  using T = f8::Tile<WM, WN, SJ, SI, KG, ST>;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[T::LDS_BYTES];
 
   uint32_t tm, tn;
   map_tile(blockIdx.x, gridDim.x, a.tiles_m, a.tiles_n, tm, tn);
   const uint32_t m0 = tm * T::BM, n0 = tn * T::BN;
   const int lane = threadIdx.x & 63;
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int grp = wave / T::GW, w = wave % T::GW;      // group along k, wave of the group
   const int wm = w / WN, wn = w % WN;
   const int half = lane >> 5, lrow = lane & 31;
-  const int steps = (int)a.KB;                // >= 1
+  uint8_t* const gsm = smem + grp * T::GROUP;
+  // This group's steps: s0 .. s0 + steps - 1 of the KB (>= 1), whole scale words with
+  // several groups.
+  const int KB = (int)a.KB, walk = KG == 1 ? KB : ((KB + KG - 1) / KG + 3) & ~3;
+  const int s0 = grp * walk, steps = max(min(KB - s0, walk), 0), W0 = s0 >> 2, words = (steps + 3) >> 2;
 
   f32x16 acc[SI][SJ];
 #pragma unroll
@@ -160,8 +171,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8GemmArgs a) 
   // Lane l fills slot l % 8 of row l / 8 of its eight; the swizzle of the odd
   // eights differs by 4, i.e. by 64 bytes of the row.
   const uint32_t chunk = (lane & 7) ^ ((lane >> 4) & 3);
-  const uint32_t a_off = (m0 + T::A_LOADS * 8 * w + (lane >> 3)) * a.KB * 128u + chunk * 16u;
-  const uint32_t b_off = (n0 + T::B_LOADS * 8 * w + (lane >> 3)) * a.KB * 128u + chunk * 16u;
+  const uint32_t a_off = ((m0 + T::A_LOADS * 8 * w + (lane >> 3)) * a.KB + s0) * 128u + chunk * 16u;
+  const uint32_t b_off = ((n0 + T::B_LOADS * 8 * w + (lane >> 3)) * a.KB + s0) * 128u + chunk * 16u;
   constexpr int LOADS = T::A_LOADS + T::B_LOADS;
   // loads [from, to) of this wave's share of step s, into stage st
   auto issue = [&](int s, int st, int from, int to) __attribute__((always_inline)) {
@@ -174,30 +185,34 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8GemmArgs a) 
       const int j = i < T::A_LOADS ? i : i - T::A_LOADS;
       const uint32_t more_off = 8u * j * a.KB * 128u + s * 128u;
       if (i < T::A_LOADS)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(smem + T::A_OFF + st * T::A_STAGE + (T::A_LOADS * w + j) * 1024), 16,
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(gsm + T::A_OFF + st * T::A_STAGE + (T::A_LOADS * w + j) * 1024), 16,
                                                  (a_off ^ (64u * (j & 1))) + more_off, 0, 0, 0);
       else
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(smem + T::B_OFF + st * T::B_STAGE + (T::B_LOADS * w + j) * 1024), 16,
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(gsm + T::B_OFF + st * T::B_STAGE + (T::B_LOADS * w + j) * 1024), 16,
                                                  (b_off ^ (64u * (j & 1))) + more_off, 0, 0, 0);
     }
   };
 
-  // ---- scales: thread t brings the words of rows t (and t + THREADS) of A's rows followed by B's
+  // ---- scales: thread t of the group brings the words of rows t (and t + 64 GW ..) of
+  // A's rows followed by B's
   auto load_scales = [&](int W, uint32_t (&v)[T::S_LOADS]) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < T::S_LOADS; ++i) {
-      const int row0 = i * T::THREADS + 64 * w;        // uniform; BM is a multiple of 64
-      const bool of_a = row0 < T::BM, any = W < (int)a.KW;
+      const int row0 = 64 * (i * T::GW + w);           // uniform; BM is a multiple of 64
+      const bool of_a = row0 < T::BM, any = W < words;
       const __amdgpu_buffer_rsrc_t rs =
           of_a ? make_rsrc(a.As, any ? a.as_bytes : 0u) : make_rsrc(a.Bs, any ? a.bs_bytes : 0u);
       const uint32_t row = of_a ? (m0 + row0 + lane) >> a.ash : (n0 + (row0 - T::BM) + lane) >> a.bsh;
-      v[i] = ld_b32(rs, (row * a.KW + W) * 4u);
+      v[i] = ld_b32(rs, (row * a.KW + W0 + W) * 4u);
     }
   };
   auto put_scales = [&](int W, const uint32_t (&v)[T::S_LOADS]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < T::S_LOADS; ++i)
-      *reinterpret_cast<uint32_t*>(smem + T::S_OFF + (W & 1) * T::S_BUF + (i * T::THREADS + 64 * w + lane) * 4) = v[i];
+    for (int i = 0; i < T::S_LOADS; ++i) {
+      const int row = 64 * (i * T::GW + w) + lane;
+      if ((T::BM + T::BN) % (64 * T::GW) == 0 || row < T::BM + T::BN)
+        *reinterpret_cast<uint32_t*>(gsm + T::S_OFF + (W & 1) * T::S_BUF + row * 4) = v[i];
+    }
   };
 
   // ---- LDS fragment addresses: row lrow, chunk 4 ks + 2 half + (0, 1) ------------------
@@ -207,9 +222,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8GemmArgs a) 
   // ---- main loop ---------------------------------------------------------------------
   // Step s, quarters (k-half, half of A's rows) (0,0) (0,1) (1,0) (1,1): each reads
   // the next quarter's operands, then multiplies.  The one barrier comes before the
-  // last quarter, after this wave's loads of step s + 1 have landed and its reads
-  // of step s are done: from there on stage s + 1 may be read and stage s
-  // overwritten.
+  // last quarter, after this wave's loads of step s + 1 have landed (those of the ST - 2
+  // later steps may be under way) and its reads of step s are done: from there on
+  // stage s + 1 may be read and stage s overwritten.
   // this tile's bias (zeros past N or without one): its bits now, fp32 into LDS later
   const __amdgpu_buffer_rsrc_t rbias = make_rsrc(a.bias, a.bias_dt >= 0 ? a.bias_bytes : 0u);
   const uint32_t bias_n = n0 + threadIdx.x;
@@ -219,7 +234,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8GemmArgs a) 
   else bias = ld_b16(rbias, bias_ok ? bias_n * 2u : kOOB);
   uint32_t snext[T::S_LOADS];
   load_scales(0, snext);
-  issue(0, 0, 0, LOADS);
+#pragma unroll
+  for (int s = 0; s < ST - 1; ++s) issue(s, s, 0, LOADS);
   put_scales(0, snext);
   if (threadIdx.x < T::BN)
     *reinterpret_cast<float*>(smem + T::BIAS_OFF + threadIdx.x * 4) =
@@ -230,7 +246,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8GemmArgs a) 
   f8::Frag fa[2][HJ], fb[2][SI];                       // by half of A's rows; by k-half
   uint32_t wa[2][SJ], wb[2][SI];                       // scale words, by parity of the word
   auto frag = [&](uint32_t at) __attribute__((always_inline)) {
-    return f8::Frag{*reinterpret_cast<const u32x4*>(smem + at), *reinterpret_cast<const u32x4*>(smem + (at ^ 16u))};
+    return f8::Frag{*reinterpret_cast<const u32x4*>(gsm + at), *reinterpret_cast<const u32x4*>(gsm + (at ^ 16u))};
   };
   auto read_a = [&](int ks, int p, int st) __attribute__((always_inline)) {
 #pragma unroll
@@ -241,24 +257,24 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8GemmArgs a) 
     for (int i = 0; i < SI; ++i) fb[ks][i] = frag((b_rd ^ (64u * ks)) + st * T::B_STAGE + i * 4096);
   };
   auto read_scales = [&](int W, int odd) __attribute__((always_inline)) {
-    const uint8_t* sp = smem + sc_rd + (W & 1) * T::S_BUF;
+    const uint8_t* sp = gsm + sc_rd + (W & 1) * T::S_BUF;
 #pragma unroll
     for (int i = 0; i < SI; ++i) wb[odd][i] = *reinterpret_cast<const uint32_t*>(sp + (T::BM + wn * 32 * SI + i * 32) * 4);
 #pragma unroll
     for (int j = 0; j < SJ; ++j) wa[odd][j] = *reinterpret_cast<const uint32_t*>(sp + (wm * 32 * SJ + j * 32) * 4);
   };
   auto join = [&]() __attribute__((always_inline)) {
-    __builtin_amdgcn_s_waitcnt(f8::wait_vm(0));
+    __builtin_amdgcn_s_waitcnt(f8::wait_vm((ST - 2) * LOADS));
     __builtin_amdgcn_s_waitcnt(f8::WAIT_LGKM0);
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_barrier();
+    if constexpr (T::GW > 1) __builtin_amdgcn_s_barrier();   // (a group of one wave shares nothing)
     __builtin_amdgcn_sched_barrier(0);
   };
   join();
   read_scales(0, 0);
   read_b(0, 0);
   read_a(0, 0, 0);
-  issue(1, 1, 0, LOADS / 2);
+  issue(ST - 1, ST - 1, 0, LOADS / 2);
   auto multiply = [&](int ks, int p, auto sel_c, int odd) __attribute__((always_inline)) {
     constexpr int SEL = decltype(sel_c)::value;
     __builtin_amdgcn_sched_barrier(0);
@@ -290,10 +306,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8GemmArgs a) 
   // step s (of scale word W = s / 4, parity odd), byte SEL = s % 4, stage s % 2
   auto step = [&](int s, auto sel_c, int odd) __attribute__((always_inline)) {
     constexpr int SEL = decltype(sel_c)::value;
-    constexpr int st = SEL & 1;
+    constexpr int st = SEL & (ST - 1), next = (st + 1) & (ST - 1), last = (st + ST - 1) & (ST - 1);
     read_a(0, 1, st);
     if constexpr (SEL == 0) load_scales((s >> 2) + 1, snext);
-    issue(s + 1, st ^ 1, LOADS / 2, LOADS);
+    issue(s + ST - 1, last, LOADS / 2, LOADS);
     multiply(0, 0, sel_c, odd);
     read_b(1, st);
     read_a(1, 0, st);
@@ -302,10 +318,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8GemmArgs a) 
     if constexpr (SEL == 2) put_scales((s >> 2) + 1, snext);
     multiply(1, 0, sel_c, odd);
     join();
-    read_b(0, st ^ 1);                               // (past the last step: whatever is there, unused)
-    read_a(0, 0, st ^ 1);
+    read_b(0, next);                                 // (past the last step: whatever is there, unused)
+    read_a(0, 0, next);
     if constexpr (SEL == 3) read_scales((s >> 2) + 1, odd ^ 1);
-    issue(s + 2, st, 0, LOADS / 2);
+    issue(s + ST, st, 0, LOADS / 2);
     multiply(1, 1, sel_c, odd);
   };
   constexpr std::integral_constant<int, 0> b0{};
@@ -324,18 +340,35 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8GemmArgs a) 
   }
   // no direct load (of zeros) may still be writing LDS when the epilogue reuses it
   __builtin_amdgcn_s_waitcnt(f8::wait_vm(0));
-  static_assert(WM * WN * 32 * (32 * SI * Elem<DTO>::bytes + 16) <= T::BIAS_OFF, "epilogue staging");
-  tile_epilogue<DTO, WM, WN, SJ, SI>(a, smem, T::BIAS_OFF, m0, n0, acc);
+  if constexpr (KG == 1) {
+    static_assert(T::GW * 32 * (32 * SI * Elem<DTO>::bytes + 16) <= T::BIAS_OFF, "epilogue staging");
+    tile_epilogue<DTO, SJ, SI>(a, smem, T::BIAS_OFF, wave, m0 + 32 * SJ * wm, n0 + 32 * SI * wn, wn, acc);
+  } else {
+    // the groups' sums, [m][n], added in group order
+    __syncthreads();                                   // (every wave writes over the others' operands)
+#pragma unroll
+    for (int si = 0; si < SI; ++si)
+#pragma unroll
+      for (int sj = 0; sj < SJ; ++sj)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *reinterpret_cast<f32x4*>(smem + grp * T::SUMS + ((32 * sj + lrow) * T::LDR + 32 * si + 8 * g + 4 * half) * 4) =
+              f32x4{acc[si][sj][4 * g], acc[si][sj][4 * g + 1], acc[si][sj][4 * g + 2], acc[si][sj][4 * g + 3]};
+    __syncthreads();
+    SumEpilogue<DTO, T::BM, T::BN, KG, T::THREADS> e;
+    e.load(a, m0, n0);
+    e.store(a, smem, n0);
+  }
 }
 
-template <int DTO, int WM, int WN, int SJ, int SI>
+template <int DTO, int WM, int WN, int SJ, int SI, int KG, int ST>
 inline void launch_f8_tile(F8GemmArgs a, hipStream_t s) {
-  using T = f8::Tile<WM, WN, SJ, SI>;
+  using T = f8::Tile<WM, WN, SJ, SI, KG, ST>;
   a.tiles_n = (a.N + T::BN - 1) / T::BN;
   a.tiles_m = (a.M + T::BM - 1) / T::BM;
-  note_launch("gemm fp8 tile, %d m x %d n", T::BM, T::BN);
+  note_launch("gemm fp8 tile, %d m x %d n, k over %d groups of waves, %d stages", T::BM, T::BN, KG, ST);
   f8::with_formats(a.fa, a.fb, [&](auto fa_c, auto fb_c) {
-    launch_kernel(f8_tile_kernel<decltype(fa_c)::value, decltype(fb_c)::value, DTO, WM, WN, SJ, SI>, dim3(a.tiles_m * a.tiles_n),
+    launch_kernel(f8_tile_kernel<decltype(fa_c)::value, decltype(fb_c)::value, DTO, WM, WN, SJ, SI, KG, ST>, dim3(a.tiles_m * a.tiles_n),
                   dim3(T::THREADS), s, a);
   });
 }
