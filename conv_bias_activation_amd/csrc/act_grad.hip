@@ -140,6 +140,7 @@ __global__ __launch_bounds__(1024) void join_columns_kernel(JoinArgs a) {
   if (!out) return;                                    // uniform
   float v = 0.0f;
   if (col < a.n)
+#pragma unroll 8
     for (uint32_t p = w; p < a.parts; p += 16u) v += a.part[(size_t)p * a.stride + blockIdx.y * a.n + col];
   sums[w][lane] = v;
   __syncthreads();

@@ -14,53 +14,63 @@
 namespace biasact {
 
 // T threads a row (16 or 64: several rows a workgroup of 256), C chunks of eight
-// values a thread: rows of up to 8 T C values.
+// values a thread: rows of up to 8 T C values.  A workgroup walks rows with gamma and
+// beta in registers, the next row's values coming in while it works on this one.
 template <int DTX, int DTY, int T, int C>
 __global__ __launch_bounds__(T > 256 ? T : 256) void layer_norm_kernel(NormArgs a) {
   constexpr int WG = T > 256 ? T : 256, W = T > 64 ? T / 64 : 1;
   __shared__ float part[2][2 * W];
-  const uint32_t t = threadIdx.x % T, row = blockIdx.x * (WG / T) + threadIdx.x / T;
-  if (row >= a.rows) return;                           // whole rows leave; with one row a workgroup none does
-  const size_t base = (size_t)row * a.N;
-  Row8<DTX> raw[C];
+  const uint32_t t = threadIdx.x % T, step = gridDim.x * (WG / T);
+  uint32_t row = blockIdx.x * (WG / T) + threadIdx.x / T;
+  Row8<DTX> next[C];
+  auto fetch = [&](uint32_t r) __attribute__((always_inline)) {
 #pragma unroll
-  for (int c = 0; c < C; ++c) raw[c] = load_row8<DTX>(a.X, base, (c * T + t) * 8u, a.N);
-  float x[C][8], s = 0.0f, none = 0.0f;
-#pragma unroll
-  for (int c = 0; c < C; ++c)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      x[c][e] = value<DTX>(raw[c], e);
-      s += x[c][e];
-    }
-  row_sum2<T>(s, none, part[0]);
-  const float n = (float)a.N, m = s / n;
-  float d = 0.0f, q = 0.0f;
-#pragma unroll
-  for (int c = 0; c < C; ++c)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      x[c][e] = (c * T + t) * 8u + e < a.N ? x[c][e] - m : 0.0f;
-      d += x[c][e];
-      q = __builtin_fmaf(x[c][e], x[c][e], q);
-    }
-  row_sum2<T>(d, q, part[1]);
-  d /= n;
-  const float rstd = 1.0f / __builtin_sqrtf(fmaxf(q / n - d * d, 0.0f) + a.eps);
+    for (int c = 0; c < C; ++c) next[c] = load_row8<DTX>(a.X, (size_t)r * a.N, (c * T + t) * 8u, a.N);
+  };
+  if (row < a.rows) fetch(row);
+  float g[C][8], b[C][8];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const uint32_t i = (c * T + t) * 8u;
-    if (i >= a.N) continue;
-    float g[8], b[8], y[8];
-    load_vec8(a.gamma, a.dtw, i, a.N, 1.0f, g);
-    load_vec8(a.beta, a.dtw, i, a.N, 0.0f, b);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf((x[c][e] - d) * rstd, g[e], b[e]);
-    store_row8<DTY>(a.Y, base, i, a.N, y);
+    load_vec8(a.gamma, a.dtw, (c * T + t) * 8u, a.N, 1.0f, g[c]);
+    load_vec8(a.beta, a.dtw, (c * T + t) * 8u, a.N, 0.0f, b[c]);
   }
-  if (t == 0 && a.mean) {
-    a.mean[row] = m + d;
-    a.rstd[row] = rstd;
+  for (; row < a.rows; row += step) {                  // (whole rows leave; with one row a workgroup it leaves as a whole)
+    float x[C][8], s = 0.0f, none = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[c][e] = value<DTX>(next[c], e);
+        s += x[c][e];
+      }
+    if (row + step < a.rows) fetch(row + step);
+    row_sum2<T>(s, none, part[0]);
+    const float n = (float)a.N, m = s / n;
+    float d = 0.0f, q = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[c][e] = (c * T + t) * 8u + e < a.N ? x[c][e] - m : 0.0f;
+        d += x[c][e];
+        q = __builtin_fmaf(x[c][e], x[c][e], q);
+      }
+    row_sum2<T>(d, q, part[1]);
+    d /= n;
+    const float rstd = 1.0f / __builtin_sqrtf(fmaxf(q / n - d * d, 0.0f) + a.eps);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const uint32_t i = (c * T + t) * 8u;
+      if (i >= a.N) continue;
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf((x[c][e] - d) * rstd, g[c][e], b[c][e]);
+      store_row8<DTY>(a.Y, (size_t)row * a.N, i, a.N, y);
+    }
+    if (t == 0 && a.mean) {
+      a.mean[row] = m + d;
+      a.rstd[row] = rstd;
+    }
   }
 }
 
@@ -113,9 +123,10 @@ __global__ __launch_bounds__(1024) void layer_norm_long_kernel(NormArgs a) {
 
 template <int DTX, int DTY, int T, int C>
 inline void launch_norm(const NormArgs& a, hipStream_t s) {
-  constexpr int WG = T > 256 ? T : 256;
+  constexpr uint32_t WG = T > 256 ? T : 256, ONCE = WG / T, MOST = 256u * 8192u / WG;   // four times what the CUs hold at once
+  const uint32_t groups = (a.rows + ONCE - 1) / ONCE;
   note_launch("layer norm, %d threads a row, %d values a thread", T, 8 * C);
-  launch_kernel(layer_norm_kernel<DTX, DTY, T, C>, dim3((a.rows + WG / T - 1) / (WG / T)), dim3(WG), s, a);
+  launch_kernel(layer_norm_kernel<DTX, DTY, T, C>, dim3(groups < MOST ? groups : MOST), dim3(WG), s, a);
 }
 
 template <int DTX, int DTY>
@@ -126,11 +137,14 @@ inline void launch_norm_to(const NormArgs& a, hipStream_t s) {
   }
   if (a.N <= 128) return launch_norm<DTX, DTY, 16, 1>(a, s);
   if (a.N <= 512) return launch_norm<DTX, DTY, 64, 1>(a, s);
-  if (a.N <= 2048) return launch_norm<DTX, DTY, 256, 1>(a, s);
-  if (a.N <= 4096) return launch_norm<DTX, DTY, 256, 2>(a, s);
+  if (a.N <= 1024) return launch_norm<DTX, DTY, 64, 2>(a, s);
+  // With few rows more threads a row hide its latency (us: 1x4096 3.0 with 512, 3.4
+  // with 256; 2048x4096 9.9 and 9.3; 32768x2048 49 with 256, 45 with one wave).
+  const bool few = a.rows < 2048;
+  if (a.N <= 2048) return few ? launch_norm<DTX, DTY, 256, 1>(a, s) : launch_norm<DTX, DTY, 64, 4>(a, s);
+  if (a.N <= 4096) return few ? launch_norm<DTX, DTY, 512, 1>(a, s) : launch_norm<DTX, DTY, 256, 2>(a, s);
   if (a.N <= 8192) return launch_norm<DTX, DTY, 256, 4>(a, s);
-  if (a.N <= 16384) return launch_norm<DTX, DTY, 1024, 2>(a, s);
-  launch_norm<DTX, DTY, 1024, 8>(a, s);
+  launch_norm<DTX, DTY, 1024, 2>(a, s);
 }
 
 template <int DTX>
@@ -164,17 +178,36 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void layer_norm_grad_kernel(Norm
     for (int e = 0; e < 8; ++e) dg[c][e] = db[c][e] = 0.0f;
   }
   const float inv_n = 1.0f / (float)a.N;
+  // the next row's values come in while this one is worked on (AHEAD), but where
+  // 1024 threads leave no registers for them
+  constexpr bool AHEAD = T < 1024;
+  Row8<DTX> nx[C];
+  Row8<DTY> ny[C];
+  float next_mean = 0.0f, next_rstd = 0.0f;
+  auto fetch = [&](uint32_t row) __attribute__((always_inline)) {
+    next_mean = a.mean[row];
+    next_rstd = a.rstd[row];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      nx[c] = load_row8<DTX>(a.X, (size_t)row * a.N, (c * T + t) * 8u, a.N);
+      ny[c] = load_row8<DTY>(a.dY, (size_t)row * a.N, (c * T + t) * 8u, a.N);
+    }
+  };
+  const uint32_t first = blockIdx.x * G + grp, step = a.parts * G;
+  if (AHEAD && first < a.rows) fetch(first);
   int odd = 0;
-  for (uint32_t row = blockIdx.x * G + grp; row < a.rows; row += a.parts * G, odd ^= 1) {
+  for (uint32_t row = first; row < a.rows; row += step, odd ^= 1) {
     const size_t base = (size_t)row * a.N;
-    const float mean = a.mean[row], rstd = a.rstd[row];
+    if (!AHEAD) fetch(row);
+    const float mean = next_mean, rstd = next_rstd;
     Row8<DTX> rx[C];
     Row8<DTY> ry[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      rx[c] = load_row8<DTX>(a.X, base, (c * T + t) * 8u, a.N);
-      ry[c] = load_row8<DTY>(a.dY, base, (c * T + t) * 8u, a.N);
+      rx[c] = nx[c];
+      ry[c] = ny[c];
     }
+    if (AHEAD && row + step < a.rows) fetch(row + step);
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int c = 0; c < C; ++c)
@@ -303,7 +336,7 @@ inline void launch_norm_grad(const NormGradArgs& a, hipStream_t s) {
 
 template <int DTX, int DTY>
 inline void launch_norm_grad_to(const NormGradArgs& a, hipStream_t s) {
-  if (a.N > kNormGradLong) {
+  if (a.N > kNormLong) {
     launch_kernel(layer_norm_grad_long_kernel<DTX, DTY>, dim3(a.rows), dim3(1024), s, a);
     if (a.part)
       launch_kernel(layer_norm_grad_columns_kernel<DTX, DTY>, dim3((a.N + 2047u) / 2048u, a.parts), dim3(256), s, a);
@@ -317,11 +350,9 @@ inline void launch_norm_grad_to(const NormGradArgs& a, hipStream_t s) {
       return launch_norm_grad<DTX, DTY, 64, 2>(a, s);
     case 256:
       if (a.N <= 2048) return launch_norm_grad<DTX, DTY, 256, 1>(a, s);
-      if (a.N <= 4096) return launch_norm_grad<DTX, DTY, 256, 2>(a, s);
-      return launch_norm_grad<DTX, DTY, 256, 4>(a, s);
-    default:
-      if (a.N <= 16384) return launch_norm_grad<DTX, DTY, 1024, 2>(a, s);
-      return launch_norm_grad<DTX, DTY, 1024, 4>(a, s);
+      return launch_norm_grad<DTX, DTY, 256, 2>(a, s);
+    case 512: return launch_norm_grad<DTX, DTY, 512, 2>(a, s);
+    default: return launch_norm_grad<DTX, DTY, 1024, 2>(a, s);
   }
 }
 

@@ -8,12 +8,12 @@ namespace biasact {
 
 // Rows longer than this are read again for each step of a layer norm; up to it
 // a row stays in its threads' registers.
-constexpr uint32_t kNormLong = 65536u, kNormGradLong = 32768u;
+constexpr uint32_t kNormLong = 16384u;
 
 // Threads that share a row of N values in layer_norm_grad (16 to 1024), and the
 // rows that a workgroup of 256 or more then takes at once.
 inline uint32_t norm_grad_threads(uint32_t N) {
-  return N <= 128u ? 16u : N <= 1024u ? 64u : N <= 8192u ? 256u : 1024u;
+  return N <= 128u ? 16u : N <= 1024u ? 64u : N <= 4096u ? 256u : N <= 8192u ? 512u : 1024u;
 }
 inline uint32_t norm_grad_rows_at_once(uint32_t N) {
   const uint32_t t = norm_grad_threads(N);
@@ -22,9 +22,9 @@ inline uint32_t norm_grad_rows_at_once(uint32_t N) {
 
 // Workgroups that each keep the column sums of their share of the rows.
 inline uint32_t norm_grad_parts(uint32_t rows, uint32_t N) {
-  if (N > kNormGradLong) return rows < 64u ? rows : 64u;
+  if (N > kNormLong) return rows < 64u ? rows : 64u;
   const uint32_t once = norm_grad_rows_at_once(N), groups = (rows + once - 1) / once;
-  const uint32_t most = norm_grad_threads(N) >= 1024u ? 256u : 1024u;
+  const uint32_t most = norm_grad_threads(N) >= 512u ? 256u : 512u;
   return groups < most ? groups : most;
 }
 

@@ -65,7 +65,7 @@ int plan_layer_norm_grad(const void* dY, const void* X, const void* gamma, const
     return kErrInvalid;
   // in place only where the types are equal, and where no later kernel reads X and dY again
   const bool in_place = dX == X || dX == dY;
-  if ((dX == dY && p->dtx != p->dty) || (in_place && N > (int64_t)kNormGradLong)) return kErrInvalid;
+  if ((dX == dY && p->dtx != p->dty) || (in_place && N > (int64_t)kNormLong)) return kErrInvalid;
   if ((dgamma || dbeta) &&
       (!workspace || !aligned(workspace, 16) || workspace_bytes < layer_norm_grad_workspace(rows, N)))
     return kErrInvalid;

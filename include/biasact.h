@@ -357,7 +357,7 @@ int layer_norm(const void* X, const void* gamma, const void* beta, void* Y, floa
  * either needs `workspace`, a caller-owned, 16-byte aligned device buffer of at
  * least layer_norm_grad_workspace_size(rows, N) bytes that no other work in flight
  * uses (BA_ERR_INVALID without it).  dX may be X or dY itself where the types are equal
- * and N is at most 32768, but must not overlap them otherwise.  Sums are fp32, in an order that
+ * and N is at most 16384, but must not overlap them otherwise.  Sums are fp32, in an order that
  * depends on the sizes alone.  N == 0: nothing to do; rows == 0: dgamma = dbeta = 0. */
 size_t layer_norm_grad_workspace_size(int64_t rows, int64_t N);
 int layer_norm_grad(const void* dY, const void* X, const void* gamma, const float* mean,
