@@ -264,42 +264,64 @@ __global__ __launch_bounds__(256) void f8_quantize_blocks_kernel(F8QuantArgs a) 
   if (threadIdx.x < end - kb) static_cast<uint8_t*>(a.scales)[(size_t)rb * a.KW * 4u + kb + threadIdx.x] = (uint8_t)(threadIdx.x ? 0u : byte);
 }
 
-// Two neighbouring values of a row as they are stored, one word or two; `two`:
-// both are there, else the first alone where `one`.
+// Two neighbouring values of a row as they are stored, one word or two.
 template <int DT> struct Pair { uint32_t w[Elem<DT>::bytes / 2]; };
 template <int DT>
-__device__ __forceinline__ Pair<DT> load_pair(const uint8_t* p, bool one, bool two) {
+__device__ __forceinline__ Pair<DT> load_pair(__amdgpu_buffer_rsrc_t r, uint32_t off) {
   Pair<DT> v;
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(v) / 4; ++i) v.w[i] = 0;
-  if (two) {
-    __builtin_memcpy(&v, p, sizeof(v));
-  } else if (one) {
-    if constexpr (Elem<DT>::bytes == 4) v.w[0] = *reinterpret_cast<const uint32_t*>(p);
-    else v.w[0] = *reinterpret_cast<const uint16_t*>(p);
+  if constexpr (Elem<DT>::bytes == 4) {
+    const u32x2 x = ld_b64(r, off);
+    v.w[0] = x.x, v.w[1] = x.y;
+  } else {
+    v.w[0] = ld_b32(r, off);
   }
   return v;
 }
 
 // ---- X[K, rows]: blocks down the columns ------------------------------------------
-// A workgroup takes two blocks of 128 k of 128 columns: wave w the k from 32 w on, a
+// A workgroup takes NB blocks of 128 k of 128 columns: wave w the k from 32 w on, a
 // lane two columns, so that a wave reads whole lines of X.  The columns' largest
 // values (or, with a scale for 128 x 128, the tile's) meet in LDS.  Codes leave
-// through LDS too, a column's 16-byte chunk c at slot c ^ (column / 2 % 16), so
-// that sixteen lanes store 256 bytes of a column.
-template <int DT, int F8>
-__global__ __launch_bounds__(512) void f8_quantize_cols_kernel(F8QuantArgs a) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[128 * 256];
-  __shared__ uint32_t most[8][128];
+// through LDS too, a column's 16-byte chunk c at slot c ^ (column / 2 % 8 NB), so
+// that 8 NB lanes store 128 NB bytes of a column.
+template <int DT, int F8, int NB>
+__global__ __launch_bounds__(256 * NB) void f8_quantize_cols_kernel(F8QuantArgs a) {
+  constexpr uint32_t PITCH = 128u * NB, CH = 8u * NB;  // bytes and chunks of a column
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[128 * PITCH];
+  __shared__ uint32_t most[4 * NB][128];
   const uint32_t lane = threadIdx.x & 63u, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t kb = 2u * fdiv(blockIdx.x, a.div), n0 = (blockIdx.x - (kb >> 1) * a.div.div) * 128u;
+  const uint32_t d = fdiv(blockIdx.x, a.div), kb = NB * d, n0 = (blockIdx.x - d * a.div.div) * 128u;
   const uint32_t n = n0 + 2u * lane, k0 = kb * 128u + 32u * w;
+  // A pair need only be aligned for one value (the GPU runs with unaligned access
+  // on).  The lane whose first column is the row's last takes the pair before it and
+  // moves it down; a row of one column has no pair.
+  constexpr uint32_t ES = Elem<DT>::bytes;
+  const uint32_t bytes = a.K * a.rows * ES;
+  const bool last = n + 1 == a.rows && a.rows > 1;
+  const uint32_t off = n < a.rows ? (k0 * a.rows + n - (last ? 1u : 0u)) * ES : kOOB;
   Pair<DT> x[32];
+  if (a.rows > 1) {                                    // uniform
 #pragma unroll
-  for (uint32_t j = 0; j < 32; ++j) {
-    const bool row = k0 + j < a.K;
-    x[j] = load_pair<DT>(static_cast<const uint8_t*>(a.X) + ((size_t)(k0 + j) * a.rows + n) * Elem<DT>::bytes, row && n < a.rows,
-                         row && n + 1 < a.rows);
+    for (uint32_t j = 0; j < 32; ++j)
+      x[j] = load_pair<DT>(make_rsrc(a.X, k0 + j < a.K ? bytes : 0u), n < a.rows ? off + j * a.rows * ES : kOOB);
+    if (a.rows & 1u) {
+#pragma unroll
+      for (uint32_t j = 0; j < 32; ++j) {
+        if constexpr (ES == 4) {
+          x[j].w[0] = last ? x[j].w[1] : x[j].w[0];
+        } else {
+          x[j].w[0] = last ? x[j].w[0] >> 16 : x[j].w[0];
+        }
+      }
+    }
+  } else {
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(a.X, bytes);
+#pragma unroll
+    for (uint32_t j = 0; j < 32; ++j) {
+      const uint32_t at = lane == 0 && k0 + j < a.K ? (k0 + j) * ES : kOOB;
+      if constexpr (ES == 4) x[j].w[0] = ld_b32(r, at), x[j].w[1] = 0;
+      else x[j].w[0] = ld_b16(r, at);
+    }
   }
   Raw8<DT> v[2][4];
 #pragma unroll
@@ -343,7 +365,7 @@ __global__ __launch_bounds__(512) void f8_quantize_cols_kernel(F8QuantArgs a) {
         lo = patch_nonfinite<DT, F8>(v[c][2 * h], lo);
         hi = patch_nonfinite<DT, F8>(v[c][2 * h + 1], hi);
       }
-      *reinterpret_cast<u32x4*>(lds + (2 * lane + c) * 256u + (((2 * w + h) ^ (lane & 15u)) << 4)) = u32x4{lo.x, lo.y, hi.x, hi.y};
+      *reinterpret_cast<u32x4*>(lds + (2 * lane + c) * PITCH + (((2 * w + h) ^ (lane & (CH - 1u))) << 4)) = u32x4{lo.x, lo.y, hi.x, hi.y};
     }
   }
   // scale bytes: waves 0 and 4 for their blocks; the row's last block also writes its word's rest
@@ -364,10 +386,10 @@ __global__ __launch_bounds__(512) void f8_quantize_cols_kernel(F8QuantArgs a) {
   __syncthreads();
 #pragma unroll
   for (uint32_t i = 0; i < 4; ++i) {
-    const uint32_t c = 32u * i + (threadIdx.x >> 4), q = threadIdx.x & 15u;
+    const uint32_t c = 32u * i + threadIdx.x / CH, q = threadIdx.x % CH;
     if (n0 + c < a.rows && kb + (q >> 3) < a.KB)
       *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(a.codes) + ((size_t)(n0 + c) * a.KB + kb) * 128u + q * 16u) =
-          *reinterpret_cast<const u32x4*>(lds + c * 256u + ((q ^ ((c >> 1) & 15u)) << 4));
+          *reinterpret_cast<const u32x4*>(lds + c * PITCH + ((q ^ ((c >> 1) & (CH - 1u))) << 4));
   }
 }
 
@@ -434,7 +456,10 @@ void launch(F8QuantArgs a, bool along_rows, bool back, hipStream_t s) {
   if (!along_rows) {
     a.div = make_fastdiv(col_tiles);
     if (back) launch_kernel(f8_dequantize_cols_kernel<DT, F8>, dim3(col_tiles * a.KB), dim3(512), s, a);
-    else launch_kernel(f8_quantize_cols_kernel<DT, F8>, dim3(col_tiles * ((a.KB + 1u) / 2u)), dim3(512), s, a);
+    // With few workgroups a CU's own loads set the time, so each takes one block (1001
+    // rows of 333 fp16 values 3.7 us, two blocks 4.5); with many, longer stores are worth more.
+    else if (col_tiles * a.KB < 1024u) launch_kernel(f8_quantize_cols_kernel<DT, F8, 1>, dim3(col_tiles * a.KB), dim3(256), s, a);
+    else launch_kernel(f8_quantize_cols_kernel<DT, F8, 2>, dim3(col_tiles * ((a.KB + 1u) / 2u)), dim3(512), s, a);
   } else if (back) {
     a.div = make_fastdiv(a.KB * 16u);
     launch_kernel(f8_dequantize_rows_kernel<DT, F8>, dim3((a.rows * a.KB * 16u + 255u) / 256u), dim3(256), s, a);
