@@ -130,26 +130,31 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs a) {
   }
 }
 
-// 64 columns a workgroup; each of its 16 waves adds every 16th part, and the
-// waves' sums are added in order.
+// 64 columns a workgroup at a time; each of its 16 waves adds every 16th part, and
+// the waves' sums are added in order.
 __global__ __launch_bounds__(1024) void join_columns_kernel(JoinArgs a) {
-  __shared__ float sums[16][64];
+  __shared__ float sums[2][16][64];
   const uint32_t lane = threadIdx.x & 63u, w = threadIdx.x >> 6;
-  const uint32_t col = blockIdx.x * 64u + lane;
   void* const out = a.out[blockIdx.y];
   if (!out) return;                                    // uniform
-  float v = 0.0f;
-  if (col < a.n)
+  int odd = 0;
+  for (uint32_t col0 = blockIdx.x * 64u; col0 < a.n; col0 += gridDim.x * 64u, odd ^= 1) {
+    const uint32_t col = col0 + lane;
+    float v = 0.0f;
+    if (col < a.n) {
+      const float* p = a.part + (size_t)w * a.stride + (size_t)blockIdx.y * a.n + col;
 #pragma unroll 8
-    for (uint32_t p = w; p < a.parts; p += 16u) v += a.part[(size_t)p * a.stride + blockIdx.y * a.n + col];
-  sums[w][lane] = v;
-  __syncthreads();
-  if (w || col >= a.n) return;
-  v = sums[0][lane];
+      for (uint32_t i = w; i < a.parts; i += 16u, p += (size_t)16 * a.stride) v += *p;
+    }
+    sums[odd][w][lane] = v;
+    __syncthreads();                                   // (the next round's sums lie elsewhere)
+    if (w || col >= a.n) continue;
+    v = sums[odd][0][lane];
 #pragma unroll
-  for (int j = 1; j < 16; ++j) v += sums[j][lane];
-  if (a.dt == DT_F32) static_cast<float*>(out)[col] = v;
-  else static_cast<uint16_t*>(out)[col] = (uint16_t)(a.dt == DT_F16 ? narrow<DT_F16>(v) : narrow<DT_BF16>(v));
+    for (int j = 1; j < 16; ++j) v += sums[odd][j][lane];
+    if (a.dt == DT_F32) static_cast<float*>(out)[col] = v;
+    else static_cast<uint16_t*>(out)[col] = (uint16_t)(a.dt == DT_F16 ? narrow<DT_F16>(v) : narrow<DT_BF16>(v));
+  }
 }
 
 }  // namespace
@@ -167,7 +172,8 @@ int launch_act_grad(int dt, const ActGradArgs& a, hipStream_t s) {
 }
 
 void launch_join_columns(const JoinArgs& a, hipStream_t s) {
-  launch_kernel(join_columns_kernel, dim3((a.n + 63u) / 64u, a.out[1] ? 2u : 1u), dim3(1024), s, a);
+  const uint32_t blocks = (a.n + 63u) / 64u;
+  launch_kernel(join_columns_kernel, dim3(blocks < 65536u ? blocks : 65536u, a.out[1] ? 2u : 1u), dim3(1024), s, a);
 }
 
 }  // namespace biasact

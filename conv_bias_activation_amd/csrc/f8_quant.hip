@@ -415,37 +415,41 @@ __global__ __launch_bounds__(256) void f8_dequantize_rows_kernel(F8QuantArgs a) 
   }
 }
 
-// Down the columns: a lane reads 16 codes of each of two columns, a wave writes
-// whole lines of X.
+// Down the columns: a lane reads 16 codes of each of two columns, twice, a wave
+// writes whole lines of X.  (A workgroup takes 256 k, which keeps the grid of a
+// single long column within 2^32 threads.)
 template <int DT, int F8>
 __global__ __launch_bounds__(512) void f8_dequantize_cols_kernel(F8QuantArgs a) {
   const uint32_t lane = threadIdx.x & 63u, w = threadIdx.x >> 6;
-  const uint32_t kb = fdiv(blockIdx.x, a.div), n = (blockIdx.x - kb * a.div.div) * 128u + 2u * lane;
-  const uint32_t k0 = kb * 128u + 16u * w;
-  if (n >= a.rows || k0 >= a.K) return;
-  Raw8<DT> v[2][2];
-#pragma unroll
-  for (uint32_t c = 0; c < 2; ++c) {
-    const uint32_t col = min(n + c, a.rows - 1u);
-    const u32x4 q = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(a.codes) + ((size_t)col * a.KB + kb) * 128u + 16u * w);
-    const uint32_t byte = static_cast<const uint8_t*>(a.scales)[(size_t)(col >> a.sh) * a.KW * 4u + kb];
-    v[c][0] = decode8<DT, F8>(u32x2{q.x, q.y}, byte);
-    v[c][1] = decode8<DT, F8>(u32x2{q.z, q.w}, byte);
-  }
+  const uint32_t d = fdiv(blockIdx.x, a.div), n = (blockIdx.x - d * a.div.div) * 128u + 2u * lane;
   const bool two = n + 1 < a.rows;
 #pragma unroll
-  for (uint32_t j = 0; j < 16; ++j) {
-    if (k0 + j >= a.K) break;
-    uint8_t* dst = static_cast<uint8_t*>(const_cast<void*>(a.X)) + ((size_t)(k0 + j) * a.rows + n) * Elem<DT>::bytes;
-    if constexpr (Elem<DT>::bytes == 4) {
-      const u32x2 o = {v[0][j >> 3].w[j & 7], v[1][j >> 3].w[j & 7]};
-      if (two) __builtin_memcpy(dst, &o, 8);
-      else *reinterpret_cast<uint32_t*>(dst) = o.x;
-    } else {
-      const uint32_t sh = 16 * (j & 1), i = (j & 7) >> 1;
-      const uint32_t o = ((v[0][j >> 3].w[i] >> sh) & 0xffffu) | ((v[1][j >> 3].w[i] >> sh) << 16);
-      if (two) __builtin_memcpy(dst, &o, 4);
-      else *reinterpret_cast<uint16_t*>(dst) = (uint16_t)o;
+  for (uint32_t h = 0; h < 2; ++h) {
+    const uint32_t k0 = d * 256u + h * 128u + 16u * w, kb = 2u * d + h;
+    if (n >= a.rows || k0 >= a.K) return;
+    Raw8<DT> v[2][2];
+#pragma unroll
+    for (uint32_t c = 0; c < 2; ++c) {
+      const uint32_t col = min(n + c, a.rows - 1u);
+      const u32x4 q = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(a.codes) + ((size_t)col * a.KB + kb) * 128u + 16u * w);
+      const uint32_t byte = static_cast<const uint8_t*>(a.scales)[(size_t)(col >> a.sh) * a.KW * 4u + kb];
+      v[c][0] = decode8<DT, F8>(u32x2{q.x, q.y}, byte);
+      v[c][1] = decode8<DT, F8>(u32x2{q.z, q.w}, byte);
+    }
+#pragma unroll
+    for (uint32_t j = 0; j < 16; ++j) {
+      if (k0 + j >= a.K) break;
+      uint8_t* dst = static_cast<uint8_t*>(const_cast<void*>(a.X)) + ((size_t)(k0 + j) * a.rows + n) * Elem<DT>::bytes;
+      if constexpr (Elem<DT>::bytes == 4) {
+        const u32x2 o = {v[0][j >> 3].w[j & 7], v[1][j >> 3].w[j & 7]};
+        if (two) __builtin_memcpy(dst, &o, 8);
+        else *reinterpret_cast<uint32_t*>(dst) = o.x;
+      } else {
+        const uint32_t sh = 16 * (j & 1), i = (j & 7) >> 1;
+        const uint32_t o = ((v[0][j >> 3].w[i] >> sh) & 0xffffu) | ((v[1][j >> 3].w[i] >> sh) << 16);
+        if (two) __builtin_memcpy(dst, &o, 4);
+        else *reinterpret_cast<uint16_t*>(dst) = (uint16_t)o;
+      }
     }
   }
 }
@@ -455,7 +459,7 @@ void launch(F8QuantArgs a, bool along_rows, bool back, hipStream_t s) {
   const uint32_t col_tiles = (a.rows + 127u) / 128u;
   if (!along_rows) {
     a.div = make_fastdiv(col_tiles);
-    if (back) launch_kernel(f8_dequantize_cols_kernel<DT, F8>, dim3(col_tiles * a.KB), dim3(512), s, a);
+    if (back) launch_kernel(f8_dequantize_cols_kernel<DT, F8>, dim3(col_tiles * ((a.KB + 1u) / 2u)), dim3(512), s, a);
     // With few workgroups a CU's own loads set the time, so each takes one block (1001
     // rows of 333 fp16 values 3.7 us, two blocks 4.5); with many, longer stores are worth more.
     else if (col_tiles * a.KB < 1024u) launch_kernel(f8_quantize_cols_kernel<DT, F8, 1>, dim3(col_tiles * a.KB), dim3(256), s, a);

@@ -160,7 +160,7 @@ enum { kF8Stream16, kF8Stream32, kF8Wave32, kF8Wave64, kF8TileDeep, kF8TileTwice
 
 inline int f8_choice(const F8GemmArgs& a, bool large) {
   const uint64_t k = a.KB;
-  if (k == 0) return kF8Stream16;                      // whose waves then have nothing to add
+  if (k == 0) return kF8TileTwice;                     // nothing to add; its grid takes any M and N
   const auto rounds = [](uint64_t tiles, uint64_t per) { return (tiles + per - 1) / per; };
   const uint64_t t16 = f8_tiles(a, 16, 16), t32 = f8_tiles(a, 16, 32), w32 = f8_tiles(a, 64, 32), w64 = f8_tiles(a, 64, 64);
   const uint64_t t128 = f8_tiles(a, 128, 128), t256 = f8_tiles(a, 256, 256);

@@ -151,7 +151,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, (f8::Tile<WM, WN, SJ, SI, KG, ST
   const int wm = w / WN, wn = w % WN;
   const int half = lane >> 5, lrow = lane & 31;
   uint8_t* const gsm = smem + grp * T::GROUP;
-  // This group's steps: s0 .. s0 + steps - 1 of the KB (>= 1), whole scale words with
+  // This group's steps: s0 .. s0 + steps - 1 of the KB (none for K = 0), whole scale words with
   // several groups.
   const int KB = (int)a.KB, walk = KG == 1 ? KB : ((KB + KG - 1) / KG + 3) & ~3;
   const int s0 = grp * walk, steps = max(min(KB - s0, walk), 0), W0 = s0 >> 2, words = (steps + 3) >> 2;

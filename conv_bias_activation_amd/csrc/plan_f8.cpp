@@ -78,7 +78,7 @@ int plan_f8_gemm(const void* A, const void* As, int a_block_rows, const void* B,
   const int64_t so = elem_bytes(out);
   p->empty = M == 0 || N == 0;
   if (p->empty) return kOk;
-  if (too_large(N * so, M)) return kErrUnsupported;
+  if (too_large(N * so, M) || (bias && too_large(N, elem_bytes(dtb)))) return kErrUnsupported;
   int64_t ab, asb, bb, bsb;
   int rc = check_packed(A, As, M, K, a_block_rows, &ab, &asb);
   if (rc) return rc;

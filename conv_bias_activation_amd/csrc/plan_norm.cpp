@@ -25,6 +25,7 @@ int norm_common(int64_t rows, int64_t N, uint32_t dtypes, NormPlan* p) {
   if (!valid_float_dt(p->dtx) || !valid_float_dt(p->dtw) || !valid_float_dt(p->dty) || ((dtypes >> 16) & 0xffu)) return kErrUnsupported;
   const int es = elem_bytes(p->dtx) > elem_bytes(p->dty) ? elem_bytes(p->dtx) : elem_bytes(p->dty);
   if (rows >= kMaxBytes || N >= kMaxBytes || too_large(rows * es, N)) return kErrUnsupported;
+  if (too_large(N, elem_bytes(p->dtw)) || too_large(rows, 4)) return kErrUnsupported;   // weights, statistics
   p->empty = rows == 0 || N == 0;
   p->rows = (uint32_t)rows;
   p->N = (uint32_t)N;
@@ -84,6 +85,7 @@ int plan_bias_act_grad(const void* dY, const void* Z, const void* dZ, const void
   p->dtb = (int)((dtypes >> 16) & 0xffu);
   if (!valid_float_dt(p->dt) || !valid_float_dt(p->dtb) || ((dtypes >> 8) & 0xffu) || (dtypes >> 24)) return kErrUnsupported;
   if (M >= kMaxBytes || N >= kMaxBytes || too_large(M * elem_bytes(p->dt), N)) return kErrUnsupported;
+  if (dbias && too_large(N, elem_bytes(p->dtb))) return kErrUnsupported;
   p->M = (uint32_t)M;
   p->N = (uint32_t)N;
   p->empty = M == 0 || N == 0;

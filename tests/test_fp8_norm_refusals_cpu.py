@@ -83,7 +83,8 @@ GEMM_BAD = [(dict(M=-1), INVALID), (dict(N=-1), INVALID), (dict(K=-1), INVALID),
             (dict(dt=dts(MX, E4, F32, BF16)), UNSUPPORTED), (dict(dt=dts(E4, BF16, F32, BF16)), UNSUPPORTED),
             (dict(dt=dts(E4, E4, I32, BF16)), UNSUPPORTED), (dict(dt=dts(E4, E4, F32, I32)), UNSUPPORTED), (dict(dt=dts(E4, E4, F32, E4)), UNSUPPORTED),
             (dict(M=2 ** 31), UNSUPPORTED), (dict(N=2 ** 31), UNSUPPORTED), (dict(K=2 ** 31), UNSUPPORTED),
-            (dict(M=2 ** 15, N=2 ** 15), UNSUPPORTED), (dict(M=2 ** 16, K=2 ** 15), UNSUPPORTED), (dict(N=2 ** 16, K=2 ** 15), UNSUPPORTED)]
+            (dict(M=2 ** 15, N=2 ** 15), UNSUPPORTED), (dict(M=2 ** 16, K=2 ** 15), UNSUPPORTED), (dict(N=2 ** 16, K=2 ** 15), UNSUPPORTED),
+            (dict(M=1, N=2 ** 29, K=0), UNSUPPORTED)]
 
 
 @pytest.mark.parametrize("residual", [False, True])
@@ -117,7 +118,7 @@ NORM_BAD = [(dict(rows=-1), INVALID), (dict(N=-1), INVALID), (dict(eps=-1e-9), I
             (dict(mean=P + 2), INVALID), (dict(rstd=P + 2), INVALID), (dict(Y=P), INVALID), (dict(dt=dts(I8, F32, 0, F16)), UNSUPPORTED),
             (dict(dt=dts(F16, I32, 0, F16)), UNSUPPORTED), (dict(dt=dts(F16, F32, 0, E4)), UNSUPPORTED), (dict(dt=dts(F16, F32, 1, F16)), UNSUPPORTED),
             (dict(rows=2 ** 31), UNSUPPORTED), (dict(N=2 ** 31), UNSUPPORTED), (dict(rows=2 ** 15, N=2 ** 15), UNSUPPORTED),
-            (dict(rows=2 ** 15, N=2 ** 14, dt=dts(F16, F32, 0, F32)), UNSUPPORTED)]
+            (dict(rows=1, N=2 ** 29), UNSUPPORTED), (dict(rows=2 ** 29, N=1), UNSUPPORTED), (dict(rows=2 ** 15, N=2 ** 14, dt=dts(F16, F32, 0, F32)), UNSUPPORTED)]
 
 
 @pytest.mark.parametrize("bad,status", NORM_BAD)
@@ -147,7 +148,8 @@ AG_BAD = [(dict(M=-1), INVALID), (dict(N=-1), INVALID), (dict(act=6), INVALID), 
           (dict(Z=None), INVALID), (dict(dZ=None, db=None), INVALID), (dict(ws=None), INVALID), (dict(ws=P + 4), INVALID), (dict(n=4 * 200 - 1), INVALID),
           (dict(dY=P + 1), INVALID), (dict(Z=P + 1), INVALID), (dict(dZ=P + 1), INVALID), (dict(db=P + 2), INVALID),
           (dict(dt=dts(I8, 0, F32)), UNSUPPORTED), (dict(dt=dts(BF16, 0, I32)), UNSUPPORTED), (dict(dt=dts(BF16, 1, F32)), UNSUPPORTED),
-          (dict(dt=dts(BF16, 0, F32, 1)), UNSUPPORTED), (dict(M=2 ** 15, N=2 ** 15), UNSUPPORTED)]
+          (dict(dt=dts(BF16, 0, F32, 1)), UNSUPPORTED), (dict(M=2 ** 15, N=2 ** 15), UNSUPPORTED),
+          (dict(M=1, N=2 ** 29), UNSUPPORTED)]
 
 
 @pytest.mark.parametrize("bad,status", AG_BAD)
