@@ -145,18 +145,21 @@ inline void launch_f8_stream(F8GemmArgs a, hipStream_t s) {
 //   stream 16x16          8x4096x4096 4.2, 16x4096x16384 12.7, 64x4096x4096 10.9, 256x4096x1024 15.9
 //   stream 32 n x 16 m    32x4096x4096 5.3, 64x4096x4096 9.0
 //   wave   64 m x 32 n    64x4096x4096 7.1, 256x4096x4096 13.6, 64x1024x16384 16.4
-//   wave   64x64          64x4096x4096 9.2, 256x4096x4096 10.5, 512x4096x4096 20.0
+//   wave   64x64          64x4096x4096 9.1, 256x4096x4096 10.6, 256x4096x8192 17.3, 512x4096x4096 20.1
+//   tile   64x64          64x4096x512 4.5, 256x4096x1024 5.5, 256x4096x4096 10.1, 256x4096x8192 18.2,
+//                         1001x1503x333 5.9 (128x128: 6.9), 512x4096x4096 15.4, 1024x4096x1024 11.7
 //   tile   128x128 deep   256x4096x4096 15.7, 512x4096x4096 16.4, 1024x4096x4096 21.0
-//   tile   128x128 twice  512x4096x4096 22.1, 1024x4096x4096 24.3, 2048x4096x4096 35
-//   tile   256x256        1024x4096x4096 38, 2048x4096x4096 41, 4096x4096x4096 57
-// (wave: each wave of four has a part of k; deep: one workgroup a CU with four
-// stages, for products of one round, whose step would else be a load's latency:
-// 4096x1024x32768 129, two stages 180; twice: two workgroups a CU.)
+//   tile   128x128 twice  1024x4096x1024 8.3, 1024x4096x4096 24.4, 2048x4096x4096 35, 4096x4096x128 13.5
+//   tile   256x256        1024x4096x4096 38, 2048x4096x4096 41, 4096x4096x4096 57, 4096x4096x128 11.3
+// (wave: each wave of four has a part of k; tile 64x64: two waves, four stages, two
+// workgroups a CU; deep: one workgroup a CU with four stages, for products of one
+// round, whose step would else be a load's latency: 4096x1024x32768 124, two stages
+// 180; twice: two workgroups a CU.)
 inline uint64_t f8_tiles(const F8GemmArgs& a, uint32_t bm, uint32_t bn) {
   return (uint64_t)((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn);
 }
 
-enum { kF8Stream16, kF8Stream32, kF8Wave32, kF8Wave64, kF8TileDeep, kF8TileTwice, kF8TileLarge };
+enum { kF8Stream16, kF8Stream32, kF8Wave32, kF8Wave64, kF8Tile64, kF8TileDeep, kF8TileTwice, kF8TileLarge };
 
 inline int f8_choice(const F8GemmArgs& a, bool large) {
   const uint64_t k = a.KB;
@@ -164,17 +167,18 @@ inline int f8_choice(const F8GemmArgs& a, bool large) {
   const auto rounds = [](uint64_t tiles, uint64_t per) { return (tiles + per - 1) / per; };
   const uint64_t t16 = f8_tiles(a, 16, 16), t32 = f8_tiles(a, 16, 32), w32 = f8_tiles(a, 64, 32), w64 = f8_tiles(a, 64, 64);
   const uint64_t t128 = f8_tiles(a, 128, 128), t256 = f8_tiles(a, 256, 256);
-  const uint64_t rest128 = t128 % 512, rest256 = t256 % 256;
-  uint64_t cost[7];
+  const uint64_t rest64 = w64 % 512, rest128 = t128 % 512, rest256 = t256 % 256;
+  uint64_t cost[8];
   cost[kF8Stream16] = 250 + 7 * k + (t16 > 256 ? (t16 - 256) * (k > 11 ? 7 * k : 80) / 256 : 0);
   cost[kF8Stream32] = rounds(t32, 256) * (250 + 9 * k);
   cost[kF8Wave32] = rounds(w32, 256) * (370 + 10 * k);
   cost[kF8Wave64] = rounds(w64, 256) * (550 + 16 * k);
+  cost[kF8Tile64] = w64 / 512 * (450 + 34 * k) + (rest64 == 0 ? 0 : rest64 <= 256 ? 390 + 19 * k : 450 + 34 * k);
   cost[kF8TileDeep] = rounds(t128, 256) * (500 + (t128 <= 128 ? 34 : 50) * k);
-  cost[kF8TileTwice] = t128 / 512 * (400 + 98 * k) + (rest128 == 0 ? 0 : rest128 <= 256 ? 400 + 62 * k : 400 + 98 * k);
+  cost[kF8TileTwice] = t128 / 512 * (500 + 95 * k) + (rest128 == 0 ? 0 : rest128 <= 256 ? 400 + 62 * k : 500 + 95 * k);
   cost[kF8TileLarge] = t256 / 256 * (1000 + 146 * k) + (rest256 == 0 ? 0 : rest256 <= 128 ? 900 + 92 * k : 1000 + 146 * k);
   int best = 0;
-  for (int i = 1; i < (large ? 7 : 6); ++i)
+  for (int i = 1; i < (large ? 8 : 7); ++i)
     if (cost[i] < cost[best]) best = i;
   return best;
 }
@@ -187,6 +191,7 @@ inline void launch_gemm_f8(const F8GemmArgs& a, hipStream_t s) {
     case kF8Stream32: return launch_f8_stream<DTO, 2, 1, 2>(a, s);
     case kF8Wave32: return launch_f8_tile<DTO, 1, 1, 2, 1, 4, 2>(a, s);
     case kF8Wave64: return launch_f8_tile<DTO, 1, 1, 2, 2, 4, 2>(a, s);
+    case kF8Tile64: return launch_f8_tile<DTO, 1, 2, 2, 1, 1, 4>(a, s);
     case kF8TileDeep: return launch_f8_tile<DTO, 2, 2, 2, 2, 1, 4>(a, s);
     case kF8TileTwice: return launch_f8_tile<DTO, 2, 2, 2, 2, 1, 2>(a, s);
     default:

@@ -118,7 +118,7 @@ struct Tile {
   static constexpr int A_OFF = 0, B_OFF = ST * A_STAGE, S_OFF = B_OFF + ST * B_STAGE, GROUP = S_OFF + 2 * S_BUF;
   static constexpr int BIAS_OFF = KG * GROUP, LDS_BYTES = BIAS_OFF + BN * 4;
   // waves a SIMD that the registers are to allow: those of two workgroups a CU, where LDS does
-  static constexpr int WAVES = THREADS / 256 * (2 * LDS_BYTES <= 160 * 1024 ? 2 : 1);
+  static constexpr int WAVES = (THREADS + 255) / 256 * (2 * LDS_BYTES <= 160 * 1024 ? 2 : 1);
   static constexpr int A_LOADS = BM / 8 / GW, B_LOADS = BN / 8 / GW;   // per wave and step
   static constexpr int S_LOADS = (BM + BN + 64 * GW - 1) / (64 * GW);  // scale words per thread
   // the sums of a tile of one wave a group, rows 4 floats apart beyond their length

@@ -325,9 +325,10 @@ def test_epilogue(ba, out, act):
                                                       ("tanh", "f32", True, False), ("sigmoid", None, False, True)])
 @pytest.mark.parametrize("M,N,K,kernel", [
     (5, 200, 1100, "stream, 16 n x 16 m"), (16, 301, 1100, "stream, 16 n x 16 m"), (32, 4096, 1100, "stream, 32 n x 16 m"), (31, 4091, 1100, "stream, 32 n x 16 m"),
-    (64, 4096, 1100, "64 m x 32 n"), (49, 4081, 1100, "64 m x 32 n"), (256, 4096, 1100, "64 m x 64 n"), (200, 4035, 1100, "64 m x 64 n"),
-    (500, 4096, 1100, "128 m x 128 n, k over 1 groups of waves, 4 stages"), (511, 4081, 1100, "128 m x 128 n, k over 1 groups of waves, 4 stages"),
-    (1100, 1160, 200, "128 m x 128 n, k over 1 groups of waves, 2 stages"), (1030, 1217, 200, "128 m x 128 n, k over 1 groups of waves, 2 stages"),
+    (64, 4096, 1100, "64 m x 32 n"), (49, 4081, 1100, "64 m x 32 n"), (256, 4096, 7000, "64 m x 64 n, k over 4"), (200, 4035, 7000, "64 m x 64 n, k over 4"),
+    (256, 4096, 1100, "64 m x 64 n, k over 1"), (200, 4035, 1100, "64 m x 64 n, k over 1"), (1100, 1160, 200, "64 m x 64 n, k over 1"),
+    (900, 4096, 2200, "128 m x 128 n, k over 1 groups of waves, 4 stages"), (911, 4081, 2200, "128 m x 128 n, k over 1 groups of waves, 4 stages"),
+    (1500, 1600, 200, "128 m x 128 n, k over 1 groups of waves, 2 stages"), (1541, 1603, 200, "128 m x 128 n, k over 1 groups of waves, 2 stages"),
     (3328, 4104, 1100, "256 m x 256 n"), (3329, 4099, 1100, "256 m x 256 n")])
 def test_epilogue_of_every_kernel(ba, M, N, K, kernel, act, bias_dt, residual, pre, out):
     # rows of whole 16-byte stores and ragged ones, last tiles of few rows and columns
@@ -339,7 +340,7 @@ def test_epilogue_of_every_kernel(ba, M, N, K, kernel, act, bias_dt, residual, p
 
 @pytest.mark.parametrize("out", ["f32", "f16"])
 @pytest.mark.parametrize("K", [1, 64, 128, 129, 256, 300, 384, 512, 513, 640, 768, 1024, 1025, 1100, 1280, 1700, 2177, 4200])
-@pytest.mark.parametrize("M,N", [(4, 500), (32, 4096), (60, 4096), (250, 4000), (480, 4000), (1100, 1160), (3329, 4104)])
+@pytest.mark.parametrize("M,N", [(4, 500), (32, 4096), (60, 4096), (250, 4000), (480, 4000), (900, 4096), (1100, 1160), (1500, 1600), (3329, 4104)])
 def test_reduction_lengths(ba, M, N, K, out):
     if M > 3000 and (K < 1000 or out == "f32"):          # (the 256x256 tile: 16-bit outputs, longer reductions)
         M, N = 1400, 1500
