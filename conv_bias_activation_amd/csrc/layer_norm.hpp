@@ -13,6 +13,9 @@
 
 namespace biasact {
 
+// (Rounding can leave a variance just below zero; NaN stays NaN.)
+__device__ __forceinline__ float rstd_of(float var, float eps) { return 1.0f / __builtin_sqrtf((var < 0.0f ? 0.0f : var) + eps); }
+
 // T threads a row (16 or 64: several rows a workgroup of 256), C chunks of eight
 // values a thread: rows of up to 8 T C values.  A workgroup walks rows with gamma and
 // beta in registers, the next row's values coming in while it works on this one.
@@ -57,7 +60,7 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void layer_norm_kernel(NormArgs 
       }
     row_sum2<T>(d, q, part[1]);
     d /= n;
-    const float rstd = 1.0f / __builtin_sqrtf(fmaxf(q / n - d * d, 0.0f) + a.eps);
+    const float rstd = rstd_of(q / n - d * d, a.eps);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const uint32_t i = (c * T + t) * 8u;
@@ -105,7 +108,7 @@ __global__ __launch_bounds__(1024) void layer_norm_long_kernel(NormArgs a) {
   }
   row_sum2<1024>(d, q, part[1]);
   d /= n;
-  const float rstd = 1.0f / __builtin_sqrtf(fmaxf(q / n - d * d, 0.0f) + a.eps);
+  const float rstd = rstd_of(q / n - d * d, a.eps);
   for (uint32_t i = threadIdx.x * 8u; i < a.N; i += 8192u) {
     const Row8<DTX> v = load_row8<DTX>(a.X, base, i, a.N);
     float g[8], b[8], y[8];

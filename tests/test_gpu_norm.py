@@ -172,6 +172,16 @@ def test_norm_nonfinite_values_stay_in_their_rows(ba, N):
     assert y[bad.cuda()].isnan().all() and torch.equal(y[~bad.cuda()], y0[~bad.cuda()])
 
 
+@pytest.mark.parametrize("N", [64, 700, 4096, 9000, 70000])
+def test_statistics_of_rows_with_nonfinite_values(ba, N):
+    x = torch.randn(5, N, generator=torch.Generator().manual_seed(2)).cuda()
+    x[1, N // 2], x[2, 0], x[3, N - 1] = float("nan"), float("inf"), float("-inf")
+    y, mean, rstd = torch.empty_like(x), torch.empty(5, device="cuda"), torch.empty(5, device="cuda")
+    ba.layer_norm(x, None, None, y, mean, rstd)
+    assert not mean[1:4].isfinite().any() and rstd[1:4].isnan().all()
+    assert mean[[0, 4]].isfinite().all() and rstd[[0, 4]].isfinite().all()
+
+
 @pytest.mark.parametrize("N", [100, 4096, 70000])
 def test_norm_in_place_and_equal_bits(ba, N):
     x = rows_of(50, N, "bf16", 3).cuda()
