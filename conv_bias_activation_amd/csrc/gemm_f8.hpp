@@ -192,7 +192,12 @@ inline void launch_gemm_f8(const F8GemmArgs& a, hipStream_t s) {
     case kF8Wave32: return launch_f8_tile<DTO, 1, 1, 2, 1, 4, 2>(a, s);
     case kF8Wave64: return launch_f8_tile<DTO, 1, 1, 2, 2, 4, 2>(a, s);
     case kF8Tile64: return launch_f8_tile<DTO, 1, 2, 2, 1, 1, 4>(a, s);
-    case kF8TileDeep: return launch_f8_tile<DTO, 2, 2, 2, 2, 1, 4>(a, s);
+    case kF8TileDeep:
+      // Operands of 64 MB and more are seldom in the last-level cache (us, bf16, out of
+      // it and in it: 1024x4096x16384, 84 MB, 94 and 63, with the wave ahead 74 and 68;
+      // 1024x4096x4096, 21 MB, 29 and 19, 26 and 21).
+      if ((uint64_t)a.a_bytes + a.b_bytes >= 1u << 26) return launch_f8_tile<DTO, 2, 2, 2, 2, 1, 4, true>(a, s);
+      return launch_f8_tile<DTO, 2, 2, 2, 2, 1, 4>(a, s);
     case kF8TileTwice: return launch_f8_tile<DTO, 2, 2, 2, 2, 1, 2>(a, s);
     default:
       if constexpr (DTO != DT_F32) launch_f8_tile<DTO, 2, 4, 4, 2, 1, 2>(a, s);

@@ -354,6 +354,13 @@ def test_long_reductions(ba, M, N, K):
     run_case(ba, M, N, K, out="bf16", seed=18)
 
 
+@pytest.mark.parametrize("out,blocks", [("f32", (1, 1)), ("f16", (1, 128)), ("bf16", (128, 1))])
+@pytest.mark.parametrize("M,N,K", [(1024, 4096, 13200), (1000, 3969, 13569), (513, 6001, 10500), (4096, 1024, 13200), (130, 16000, 4200)])
+def test_large_operands_of_one_round(ba, M, N, K, out, blocks):
+    run_case(ba, M, N, K, "f8e5m2", "f8e4m3", out, "gelu", "f32", residual=True, pre=True, blocks=blocks, seed=23)
+    assert "128 m x 128 n, k over 1 groups of waves, 4 stages, a wave ahead" in ba.last_tile_config()
+
+
 @pytest.mark.parametrize("M,N,K", [(3, 70, 300), (130, 301, 260), (256, 512, 512), (1100, 1160, 300)])
 def test_outputs_aligned_for_one_value(ba, M, N, K):
     run_case(ba, M, N, K, "f8e4m3", "f8e4m3", "bf16", "gelu", "bf16", residual=True, pre=True, shift=1)
