@@ -89,7 +89,10 @@ __device__ __forceinline__ float act_grad(float dy, float z, float alpha) {
 }
 
 // A lane holds eight columns, 2^lane_bits lanes share a row, and a workgroup
-// takes 256 >> lane_bits rows at once, walking down its share of them.
+// takes 256 >> lane_bits rows at once, walking down its share of them.  Bound by
+// memory: dY and Z are read once, dZ written once.  bf16, us with the sums' join, beside
+// a large copy's time for as many bytes (4.92 TB/s): 8192x16384 GELU 156 (164), 32768x4096
+// LeakyReLU 151 (164), 1001x333 GELU fp32 7.7, two launches.
 template <int DT>
 __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs a) {
   __shared__ float cols[256][9];
@@ -131,7 +134,8 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs a) {
 }
 
 // 64 columns a workgroup at a time; each of its 16 waves adds every 16th part, and
-// the waves' sums are added in order.
+// the waves' sums are added in order.  A few MB at most, from L2: 2.3 to 5.3 us
+// (512 parts of 2 x 4096 columns 4.4 to 5.3).
 __global__ __launch_bounds__(1024) void join_columns_kernel(JoinArgs a) {
   __shared__ float sums[2][16][64];
   const uint32_t lane = threadIdx.x & 63u, w = threadIdx.x >> 6;

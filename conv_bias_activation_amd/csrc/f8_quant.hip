@@ -8,6 +8,10 @@
 // there is one rounding, and nothing saturates.  An infinity becomes NaN in e4m3
 // and stays one in e5m2, NaN stays NaN; neither counts for its block's scale.  A
 // block without another value than zero has scale byte 0.
+//
+// Every kernel here is bound by memory and reads and writes each value once.  Times
+// below are of calls replayed from a graph, beside what a large copy (4.92 TB/s, read and
+// written bytes) would take for the same bytes.
 #include "f8_launch.hpp"
 #include "launch_kernel.hpp"
 
@@ -206,7 +210,9 @@ __device__ __forceinline__ uint32_t max16(uint32_t m) {
 
 // ---- X[rows, K], a scale for each 128 values of a row -----------------------------
 // One lane per 8 values, a wave per 512 of a row: sixteen lanes make a block, and
-// lane 0 writes the four scale bytes as one word.
+// lane 0 writes the four scale bytes as one word.  32768x4096 bf16 70 us (copy 83;
+// what was written just before is still in the last-level cache), 4096x4096 fp32 13.4 (17),
+// 8x4096 bf16 2.2, which is a launch.
 template <int DT, int F8>
 __global__ __launch_bounds__(256) void f8_quantize_rows_kernel(F8QuantArgs a) {
   const uint32_t wid = blockIdx.x * 4u + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -230,7 +236,8 @@ __global__ __launch_bounds__(256) void f8_quantize_rows_kernel(F8QuantArgs a) {
 }
 
 // ---- X[rows, K], a scale for each 128 x 128 ---------------------------------------
-// A workgroup per block, sixteen lanes a row, eight rows a thread.
+// A workgroup per block, sixteen lanes a row, eight rows a thread: the block stays in
+// registers between its maximum and its codes.  4096x4096 fp16 8.4 us (copy 10.2).
 template <int DT, int F8>
 __global__ __launch_bounds__(256) void f8_quantize_blocks_kernel(F8QuantArgs a) {
   __shared__ uint32_t part[4];
@@ -279,18 +286,20 @@ __device__ __forceinline__ Pair<DT> load_pair(__amdgpu_buffer_rsrc_t r, uint32_t
 }
 
 // ---- X[K, rows]: blocks down the columns ------------------------------------------
-// A workgroup takes NB blocks of 128 k of 128 columns: wave w the k from 32 w on, a
-// lane two columns, so that a wave reads whole lines of X.  The columns' largest
-// values (or, with a scale for 128 x 128, the tile's) meet in LDS.  Codes leave
-// through LDS too, a column's 16-byte chunk c at slot c ^ (column / 2 % 8 NB), so
-// that 8 NB lanes store 128 NB bytes of a column.
-template <int DT, int F8, int NB>
-__global__ __launch_bounds__(256 * NB) void f8_quantize_cols_kernel(F8QuantArgs a) {
-  constexpr uint32_t PITCH = 128u * NB, CH = 8u * NB;  // bytes and chunks of a column
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[128 * PITCH];
-  __shared__ uint32_t most[4 * NB][128];
+// A workgroup takes 128 k of 128 columns: wave w the k from 32 w on, a lane two
+// columns, so that a wave reads whole lines of X.  The columns' largest values (or, with
+// a scale for 128 x 128, the tile's) meet in LDS.  Codes leave through LDS too, a
+// column's 16-byte chunk c at slot c ^ (column / 2 % 8), so that eight lanes store the
+// 128 bytes of a column.  4096 columns of 32768 bf16 85 us (copy 83; the same with two
+// blocks of k a workgroup), 4096x4096 fp16 in 128 x 128 9.1 (10.2), 1001 columns of
+// 333 fp16 3.7 (4.5 with two blocks), 4095 columns of 4096 fp16, whose pairs lie
+// across words every other row, 12.5.
+template <int DT, int F8>
+__global__ __launch_bounds__(256) void f8_quantize_cols_kernel(F8QuantArgs a) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[128 * 128];
+  __shared__ uint32_t most[4][128];
   const uint32_t lane = threadIdx.x & 63u, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t d = fdiv(blockIdx.x, a.div), kb = NB * d, n0 = (blockIdx.x - d * a.div.div) * 128u;
+  const uint32_t kb = fdiv(blockIdx.x, a.div), n0 = (blockIdx.x - kb * a.div.div) * 128u;
   const uint32_t n = n0 + 2u * lane, k0 = kb * 128u + 32u * w;
   // A pair need only be aligned for one value (the GPU runs with unaligned access
   // on).  The lane whose first column is the row's last takes the pair before it and
@@ -345,7 +354,7 @@ __global__ __launch_bounds__(256 * NB) void f8_quantize_cols_kernel(F8QuantArgs 
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const u32x2 o = *reinterpret_cast<const u32x2*>(&most[(w & 4u) + i][2 * lane]);
+    const u32x2 o = *reinterpret_cast<const u32x2*>(&most[i][2 * lane]);
     m[0] = max(m[0], o.x);
     m[1] = max(m[1], o.y);
   }
@@ -365,35 +374,35 @@ __global__ __launch_bounds__(256 * NB) void f8_quantize_cols_kernel(F8QuantArgs 
         lo = patch_nonfinite<DT, F8>(v[c][2 * h], lo);
         hi = patch_nonfinite<DT, F8>(v[c][2 * h + 1], hi);
       }
-      *reinterpret_cast<u32x4*>(lds + (2 * lane + c) * PITCH + (((2 * w + h) ^ (lane & (CH - 1u))) << 4)) = u32x4{lo.x, lo.y, hi.x, hi.y};
+      *reinterpret_cast<u32x4*>(lds + (2 * lane + c) * 128u + (((2 * w + h) ^ (lane & 7u)) << 4)) = u32x4{lo.x, lo.y, hi.x, hi.y};
     }
   }
-  // scale bytes: waves 0 and 4 for their blocks; the row's last block also writes its word's rest
-  const uint32_t b = kb + (w >> 2);
-  if ((w & 3u) == 0 && b < a.KB) {
+  // scale bytes; the row's last block also writes its word's rest
+  if (w == 0) {
     uint8_t* const s = static_cast<uint8_t*>(a.scales);
-    const uint32_t end = b + 1 == a.KB ? a.KW * 4u : b + 1;
+    const uint32_t end = kb + 1 == a.KB ? a.KW * 4u : kb + 1;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const bool in = a.sh ? lane == 0 && c == 0 : n + c < a.rows;
       uint8_t* const at = s + (size_t)(a.sh ? n0 >> 7 : n + c) * a.KW * 4u;
       if (in) {
-        at[b] = (uint8_t)byte[c];
-        for (uint32_t e = b + 1; e < end; ++e) at[e] = 0;
+        at[kb] = (uint8_t)byte[c];
+        for (uint32_t e = kb + 1; e < end; ++e) at[e] = 0;
       }
     }
   }
   __syncthreads();
 #pragma unroll
   for (uint32_t i = 0; i < 4; ++i) {
-    const uint32_t c = 32u * i + threadIdx.x / CH, q = threadIdx.x % CH;
-    if (n0 + c < a.rows && kb + (q >> 3) < a.KB)
+    const uint32_t c = 32u * i + (threadIdx.x >> 3), q = threadIdx.x & 7u;
+    if (n0 + c < a.rows)
       *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(a.codes) + ((size_t)(n0 + c) * a.KB + kb) * 128u + q * 16u) =
-          *reinterpret_cast<const u32x4*>(lds + c * PITCH + ((q ^ ((c >> 1) & (CH - 1u))) << 4));
+          *reinterpret_cast<const u32x4*>(lds + c * 128u + ((q ^ ((c >> 1) & 7u)) << 4));
   }
 }
 
 // ---- reading back -------------------------------------------------------------------
+// Along the rows: eight codes a lane.  32768x4096 bf16 63 to 68 us (copy 83).
 template <int DT, int F8>
 __global__ __launch_bounds__(256) void f8_dequantize_rows_kernel(F8QuantArgs a) {
   const uint32_t t = blockIdx.x * 256u + threadIdx.x;
@@ -416,7 +425,8 @@ __global__ __launch_bounds__(256) void f8_dequantize_rows_kernel(F8QuantArgs a) 
 }
 
 // Down the columns: a lane reads 16 codes of each of two columns, twice, a wave
-// writes whole lines of X.  (A workgroup takes 256 k, which keeps the grid of a
+// writes whole lines of X: 4096 columns of 32768 bf16 104 us (copy 83), 4096x4096
+// fp16 10.4 (10.2).  (A workgroup takes 256 k, which keeps the grid of a
 // single long column within 2^32 threads.)
 template <int DT, int F8>
 __global__ __launch_bounds__(512) void f8_dequantize_cols_kernel(F8QuantArgs a) {
@@ -460,10 +470,7 @@ void launch(F8QuantArgs a, bool along_rows, bool back, hipStream_t s) {
   if (!along_rows) {
     a.div = make_fastdiv(col_tiles);
     if (back) launch_kernel(f8_dequantize_cols_kernel<DT, F8>, dim3(col_tiles * ((a.KB + 1u) / 2u)), dim3(512), s, a);
-    // With few workgroups a CU's own loads set the time, so each takes one block (1001
-    // rows of 333 fp16 values 3.7 us, two blocks 4.5); with many, longer stores are worth more.
-    else if (col_tiles * a.KB < 1024u) launch_kernel(f8_quantize_cols_kernel<DT, F8, 1>, dim3(col_tiles * a.KB), dim3(256), s, a);
-    else launch_kernel(f8_quantize_cols_kernel<DT, F8, 2>, dim3(col_tiles * ((a.KB + 1u) / 2u)), dim3(512), s, a);
+    else launch_kernel(f8_quantize_cols_kernel<DT, F8>, dim3(col_tiles * a.KB), dim3(256), s, a);
   } else if (back) {
     a.div = make_fastdiv(a.KB * 16u);
     launch_kernel(f8_dequantize_rows_kernel<DT, F8>, dim3((a.rows * a.KB * 16u + 255u) / 256u), dim3(256), s, a);

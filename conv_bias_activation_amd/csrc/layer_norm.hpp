@@ -19,16 +19,21 @@ __device__ __forceinline__ float rstd_of(float var, float eps) { return 1.0f / _
 // T threads a row (16 or 64: several rows a workgroup of 256), C chunks of eight
 // values a thread: rows of up to 8 T C values.  A workgroup walks rows with gamma and
 // beta in registers, the next row's values coming in while it works on this one.
+// Bound by memory: each value is read and written once.  bf16, us, beside the time of a
+// large copy of as many bytes (4.92 TB/s): 32768x4096 95 to 100 (109; a workgroup a row 128),
+// 32768x1024 25 (27; 44), 32768x2048 45 to 53 (55), 8192x8192 47 (55), 8192x5120 43 (34),
+// 1x4096 3.0, a launch.
 template <int DTX, int DTY, int T, int C>
 __global__ __launch_bounds__(T > 256 ? T : 256) void layer_norm_kernel(NormArgs a) {
   constexpr int WG = T > 256 ? T : 256, W = T > 64 ? T / 64 : 1;
   __shared__ float part[2][2 * W];
   const uint32_t t = threadIdx.x % T, step = gridDim.x * (WG / T);
   uint32_t row = blockIdx.x * (WG / T) + threadIdx.x / T;
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.X, a.rows * a.N * Elem<DTX>::bytes);
   Row8<DTX> next[C];
   auto fetch = [&](uint32_t r) __attribute__((always_inline)) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) next[c] = load_row8<DTX>(a.X, (size_t)r * a.N, (c * T + t) * 8u, a.N);
+    for (int c = 0; c < C; ++c) next[c] = load_row8<DTX>(rx, a.X, r * a.N, (c * T + t) * 8u, a.N);
   };
   if (row < a.rows) fetch(row);
   float g[C][8], b[C][8];
@@ -77,7 +82,8 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void layer_norm_kernel(NormArgs 
   }
 }
 
-// Rows too long for registers: a workgroup a row, which it reads three times.
+// Rows too long for registers: a workgroup a row, which it reads three times, the second
+// and third time from L2 where few rows are under way.
 template <int DTX, int DTY>
 __global__ __launch_bounds__(1024) void layer_norm_long_kernel(NormArgs a) {
   __shared__ float part[2][32];
@@ -126,7 +132,10 @@ __global__ __launch_bounds__(1024) void layer_norm_long_kernel(NormArgs a) {
 
 template <int DTX, int DTY, int T, int C>
 inline void launch_norm(const NormArgs& a, hipStream_t s) {
-  constexpr uint32_t WG = T > 256 ? T : 256, ONCE = WG / T, MOST = 256u * 8192u / WG;   // four times what the CUs hold at once
+  // Four times what the CUs hold at once; with four chunks a thread, whose weights take
+  // longer to load, ten workgroups a CU (us: 8192x8192 bf16 47, with 8192 workgroups 56;
+  // 32768x4096, two chunks, 106 and 100).
+  constexpr uint32_t WG = T > 256 ? T : 256, ONCE = WG / T, MOST = C == 4 ? 2560u : 256u * 8192u / WG;
   const uint32_t groups = (a.rows + ONCE - 1) / ONCE;
   note_launch("layer norm, %d threads a row, %d values a thread", T, 8 * C);
   launch_kernel(layer_norm_kernel<DTX, DTY, T, C>, dim3(groups < MOST ? groups : MOST), dim3(WG), s, a);
@@ -142,11 +151,12 @@ inline void launch_norm_to(const NormArgs& a, hipStream_t s) {
   if (a.N <= 512) return launch_norm<DTX, DTY, 64, 1>(a, s);
   if (a.N <= 1024) return launch_norm<DTX, DTY, 64, 2>(a, s);
   // With few rows more threads a row hide its latency (us: 1x4096 3.0 with 512, 3.4
-  // with 256; 2048x4096 9.9 and 9.3; 32768x2048 49 with 256, 45 with one wave).
+  // with 256; 2048x4096 9.9 and 9.3; 64x8192 4.1 with 512, 5.0 with 256, 8192x8192 50 and
+  // 47; 32768x2048 49 with 256, 45 with one wave).
   const bool few = a.rows < 2048;
   if (a.N <= 2048) return few ? launch_norm<DTX, DTY, 256, 1>(a, s) : launch_norm<DTX, DTY, 64, 4>(a, s);
   if (a.N <= 4096) return few ? launch_norm<DTX, DTY, 512, 1>(a, s) : launch_norm<DTX, DTY, 256, 2>(a, s);
-  if (a.N <= 8192) return launch_norm<DTX, DTY, 256, 4>(a, s);
+  if (a.N <= 8192) return few ? launch_norm<DTX, DTY, 512, 2>(a, s) : launch_norm<DTX, DTY, 256, 4>(a, s);
   launch_norm<DTX, DTY, 1024, 2>(a, s);
 }
 
@@ -165,8 +175,11 @@ inline int launch_layer_norm(int dty, const NormArgs& a, hipStream_t s) {
 //   dx = rstd (g - sum(g) / N - xh sum(g xh) / N)
 //   dgamma = sum over rows of dy xh, dbeta = sum over rows of dy
 // A workgroup walks rows parts apart, T threads a row, and keeps the column sums
-// of what it has seen in registers: X and dY are read once.  Its sums go to
-// part[workgroup], which a second kernel adds up in a fixed order.
+// of what it has seen in registers: X and dY are read once, dX written once, which is
+// what bounds it.  Its sums go to part[workgroup], which a second kernel adds up in a fixed
+// order (atomics would change it).  Both kernels, us, beside the copy's time for as many
+// bytes: 32768x4096 bf16 150 to 157 (164; 175 without the next row under way), fp32 287
+// (328), 32768x1024 bf16 37 (41), 4096x16384 bf16 95 (82), 1001x1024 fp32 9.8, two launches.
 template <int DTX, int DTY, int T, int C>
 __global__ __launch_bounds__(T > 256 ? T : 256) void layer_norm_grad_kernel(NormGradArgs a) {
   constexpr int WG = T > 256 ? T : 256, G = WG / T, W = T > 64 ? T / 64 : 1;
@@ -184,6 +197,7 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void layer_norm_grad_kernel(Norm
   // the next row's values come in while this one is worked on (AHEAD), but where
   // 1024 threads leave no registers for them
   constexpr bool AHEAD = T < 1024;
+  const __amdgpu_buffer_rsrc_t bx = make_rsrc(a.X, a.rows * a.N * Elem<DTX>::bytes), by = make_rsrc(a.dY, a.rows * a.N * Elem<DTY>::bytes);
   Row8<DTX> nx[C];
   Row8<DTY> ny[C];
   float next_mean = 0.0f, next_rstd = 0.0f;
@@ -192,8 +206,9 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void layer_norm_grad_kernel(Norm
     next_rstd = a.rstd[row];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      nx[c] = load_row8<DTX>(a.X, (size_t)row * a.N, (c * T + t) * 8u, a.N);
-      ny[c] = load_row8<DTY>(a.dY, (size_t)row * a.N, (c * T + t) * 8u, a.N);
+      const uint32_t i = (c * T + t) * 8u;
+      nx[c] = AHEAD ? load_row8<DTX>(bx, a.X, row * a.N, i, a.N) : load_row8<DTX>(a.X, (size_t)row * a.N, i, a.N);
+      ny[c] = AHEAD ? load_row8<DTY>(by, a.dY, row * a.N, i, a.N) : load_row8<DTY>(a.dY, (size_t)row * a.N, i, a.N);
     }
   };
   const uint32_t first = blockIdx.x * G + grp, step = a.parts * G;

@@ -11,7 +11,8 @@ namespace biasact {
 constexpr uint32_t kNormLong = 16384u;
 
 // Threads that share a row of N values in layer_norm_grad (16 to 1024), and the
-// rows that a workgroup of 256 or more then takes at once.
+// rows that a workgroup of 256 or more then takes at once: eight or sixteen values a
+// thread, whose column sums, weights and next row just fit its registers.
 inline uint32_t norm_grad_threads(uint32_t N) {
   return N <= 128u ? 16u : N <= 1024u ? 64u : N <= 4096u ? 256u : N <= 8192u ? 512u : 1024u;
 }
@@ -20,16 +21,21 @@ inline uint32_t norm_grad_rows_at_once(uint32_t N) {
   return t >= 256u ? 1u : 256u / t;
 }
 
-// Workgroups that each keep the column sums of their share of the rows.
+// Workgroups that each keep the column sums of their share of the rows: one a CU, whose
+// next row is under way while it works on this one, or two where rows are short (us with
+// 256 and 512: 32768x4096 bf16 153 and 157, fp32 284 and 303, 4096x16384 bf16 96 and 110;
+// 32768x1024 42 and 37, 32768x256 27 and 20, 8192x1280 fp32 32 and 28; with 1024 more but
+// for 32768x256, 22).
 inline uint32_t norm_grad_parts(uint32_t rows, uint32_t N) {
   if (N > kNormLong) return rows < 64u ? rows : 64u;
   const uint32_t once = norm_grad_rows_at_once(N), groups = (rows + once - 1) / once;
-  const uint32_t most = norm_grad_threads(N) >= 512u ? 256u : 512u;
+  const uint32_t most = N <= 2048u ? 512u : 256u;
   return groups < most ? groups : most;
 }
 
 // Lanes (as a power of two) that share a row of N values in bias_act_grad, eight
-// columns a lane, and the row splits for M rows.
+// columns a lane, and the row splits for M rows: up to 1024 workgroups, four a CU (us,
+// bf16: 8192x16384 GELU 158, with 2048 171, 4096 166; 32768x4096 LeakyReLU 151, 165, 168).
 inline uint32_t act_grad_lane_bits(uint32_t N) {
   uint32_t b = 0;
   while (b < 6u && (8u << b) < N) ++b;
@@ -38,7 +44,7 @@ inline uint32_t act_grad_lane_bits(uint32_t N) {
 inline uint32_t act_grad_parts(uint32_t M, uint32_t N) {
   const uint32_t b = act_grad_lane_bits(N), tiles = (N + (8u << b) - 1) / (8u << b);
   const uint32_t once = 256u >> b;                     // rows that a workgroup takes at once
-  const uint32_t groups = (M + once - 1) / once, want = (2048u + tiles - 1) / tiles;
+  const uint32_t groups = (M + once - 1) / once, want = (1024u + tiles - 1) / tiles;
   return groups < want ? groups : want;
 }
 
