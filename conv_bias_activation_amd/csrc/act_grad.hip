@@ -92,7 +92,7 @@ __device__ __forceinline__ float act_grad(float dy, float z, float alpha) {
 // takes 256 >> lane_bits rows at once, walking down its share of them.  Bound by
 // memory: dY and Z are read once, dZ written once.  bf16, us with the sums' join, beside
 // a large copy's time for as many bytes (4.92 TB/s): 8192x16384 GELU 156 (164), 32768x4096
-// LeakyReLU 151 (164), 1001x333 GELU fp32 7.7, two launches.
+// LeakyReLU 151 (164), 1021x1003 tanh fp32 7.7, two launches.
 template <int DT>
 __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs a) {
   __shared__ float cols[256][9];

@@ -35,7 +35,7 @@ int layer_norm_grad(const void* dY, const void* X, const void* gamma, const floa
   int rc = plan_layer_norm_grad(dY, X, gamma, mean, rstd, dX, dgamma, dbeta, rows, N, dtypes, workspace, workspace_bytes, &p);
   if (rc || p.N == 0) return rc;
   const bool sums = dgamma || dbeta;
-  const uint32_t parts = p.rows ? norm_grad_parts(p.rows, p.N) : 0u;
+  const uint32_t parts = p.rows ? norm_grad_parts(p.rows, p.N, (p.dtx == DT_F32 ? 4u : 2u) + (p.dty == DT_F32 ? 4u : 2u)) : 0u;
   if (p.rows) {
     const NormGradArgs a = {dY, X, gamma, mean, rstd, dX, sums ? static_cast<float*>(workspace) : nullptr, p.rows, p.N, parts, p.dtw};
     switch (p.dtx) {

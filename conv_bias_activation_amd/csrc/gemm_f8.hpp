@@ -11,6 +11,11 @@
 // bytes, UN blocks under way (a register of each would allow two); chunk c of row
 // r lies at slot c ^ (r / 2 % 8).  Lane (r, g) takes the chunks g and 4 + g of row r:
 // any assignment will do that is the same for both operands, since a block has one scale.
+//
+// Bound by the latency of loads and by reading B (8x4096x4096 bf16 4.2 us, of which a
+// launch 1.6 and B's 16.8 MB at 4.9 TB/s 3.4; 16x4096x16384 12.7; 8x16384x4096 12.4).  With 3
+// or 4 blocks under way the LDS holds one workgroup a CU: 8x4096x4096 4.3, 32x4096x4096 7.7
+// instead of 6.6; blocks dealt to the waves in turn made no difference.
 #pragma once
 
 #include "gemm_f8_tile.hpp"
@@ -194,8 +199,8 @@ inline void launch_gemm_f8(const F8GemmArgs& a, hipStream_t s) {
     case kF8Tile64: return launch_f8_tile<DTO, 1, 2, 2, 1, 1, 4>(a, s);
     case kF8TileDeep:
       // Operands of 64 MB and more are seldom in the last-level cache (us, bf16, out of
-      // it and in it: 1024x4096x16384, 84 MB, 94 and 63, with the wave ahead 74 and 68;
-      // 1024x4096x4096, 21 MB, 29 and 19, 26 and 21).
+      // it and in it: 1024x4096x16384, 84 MB, 90 and 63, with the wave ahead 70 and 68;
+      // 1024x4096x4096, 21 MB, 26 and 19, 23 and 21).
       if ((uint64_t)a.a_bytes + a.b_bytes >= 1u << 26) return launch_f8_tile<DTO, 2, 2, 2, 2, 1, 4, true>(a, s);
       return launch_f8_tile<DTO, 2, 2, 2, 2, 1, 4>(a, s);
     case kF8TileTwice: return launch_f8_tile<DTO, 2, 2, 2, 2, 1, 2>(a, s);

@@ -5,7 +5,7 @@
 // SJ x SI accumulator blocks of 32x32 each: an output tile of 32 SJ WM (m) x 32 SI WN
 // (n).  A k-step is one block of 128 values: a whole cache line per row and one scale.
 //
-// Codes reach LDS without passing through registers, 16 bytes a lane, two
+// Codes reach LDS without passing through registers, 16 bytes a lane, ST
 // stages deep; chunk c of row r lies at slot c ^ (r / 2 % 8).  The matrix
 // instruction v_mfma_scale_f32_32x32x64 applies both scales itself; within a
 // block all k share them, so any assignment of the block's k to instructions and
@@ -14,6 +14,14 @@
 // A word of four scale bytes serves four steps; the words travel through
 // registers into LDS, one word a row, and the instruction's operand selector
 // picks the step's byte.
+//
+// What bounds it: the 256x256 tile's step takes 1.4 us, 3.1 PFLOP/s, against 2.9 to 3.5
+// of the matrix instructions alone on random operands (power); three quarters of its
+// cycles are LDS reads of operands, without conflicts that matter, a quarter direct loads.
+// Round it lie 10 us of first loads, epilogue and stores.  bf16 outputs: 4096^3 55 us (2490
+// TFLOP/s), with GELU 62, 4096x4096x16384 188 (2920), 8192^3 377 to 386 (2850 to 2920), 32768x1024x4096
+// 105 (2630); fp32 outputs 4096^3 108 to 114.  Four waves of 128x128 63 (one wave a
+// SIMD hides nothing), all loads of a step at once 57, other priorities the same.
 //
 // Registers: 128 sums a lane at 4 x 2 blocks, and the operands of two quarters of
 // a step: a quarter multiplies one k-half of half the wave's rows of A by all its
@@ -57,9 +65,9 @@ __device__ __forceinline__ f32x4 mfma16(const Frag& b, const Frag& a, f32x4 acc,
 }
 
 // ---- products whose sums are to be fp32 throughout -----------------------------------
-// The 8-bit instructions above add eight neighbouring products in fixed point: what
-// lies 2^14 or more below the leading bit that the largest of the eight can have
-// is cut off (measured on single products: 2^2 beside 2^16 vanishes, 2^3 stays), which
+// The 8-bit instructions above add eight neighbouring products in fixed point: each is
+// cut off below 2^(e - 13), e the largest sum of two exponents among the eight
+// (measured on single products: 2^2 beside 2^16 vanishes, 2^3 stays), which
 // leaves a result of many terms 5e-5 off (2-norm) without a bias.  A 16-bit output rounds
 // by 2e-4 or more; an fp32 output would show it, so there the codes are widened
 // to bf16 with their scale, which is exact within bf16's range, and bf16
@@ -142,7 +150,7 @@ constexpr int wait_vm(int n) { return 0x0F70 | (n & 0xF) | ((n >> 4) << 14); }
 // at once, which HBM gives faster than one every step, and only the workgroup's share
 // of them, since an XCD that works on 8 x 4 tiles wants each line of A four times and
 // each of B eight times.  (Where it works on others, some lines come late, as without.)
-// 4096x1024x32768 with the operands out of the last-level cache 198 -> 155 us, from
+// 4096x1024x32768 with the operands out of the last-level cache 195 -> 152 us, from
 // it 129 -> 141.  (The others' own loads, three steps ahead, would have to be waited for
 // in order; this wave waits for none.)
 template <int FA, int FB, int DTO, int WM, int WN, int SJ, int SI, int KG, int ST, bool AHEAD>
@@ -335,7 +343,7 @@ __global__ __launch_bounds__(64 * (WM * WN * KG + AHEAD), (AHEAD ? 1 : f8::Tile<
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-  // step s (of scale word W = s / 4, parity odd), byte SEL = s % 4, stage s % 2
+  // step s (of scale word W = s / 4, parity odd), byte SEL = s % 4, stage s % ST
   auto step = [&](int s, auto sel_c, int odd) __attribute__((always_inline)) {
     constexpr int SEL = decltype(sel_c)::value;
     constexpr int st = SEL & (ST - 1), next = (st + 1) & (ST - 1), last = (st + ST - 1) & (ST - 1);

@@ -178,7 +178,7 @@ inline int launch_layer_norm(int dty, const NormArgs& a, hipStream_t s) {
 // of what it has seen in registers: X and dY are read once, dX written once, which is
 // what bounds it.  Its sums go to part[workgroup], which a second kernel adds up in a fixed
 // order (atomics would change it).  Both kernels, us, beside the copy's time for as many
-// bytes: 32768x4096 bf16 150 to 157 (164; 175 without the next row under way), fp32 287
+// bytes: 32768x4096 bf16 150 to 157 (164; 175 without the next row under way), fp32 285
 // (328), 32768x1024 bf16 37 (41), 4096x16384 bf16 95 (82), 1001x1024 fp32 9.8, two launches.
 template <int DTX, int DTY, int T, int C>
 __global__ __launch_bounds__(T > 256 ? T : 256) void layer_norm_grad_kernel(NormGradArgs a) {

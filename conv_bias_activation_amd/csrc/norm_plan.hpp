@@ -21,15 +21,16 @@ inline uint32_t norm_grad_rows_at_once(uint32_t N) {
   return t >= 256u ? 1u : 256u / t;
 }
 
-// Workgroups that each keep the column sums of their share of the rows: one a CU, whose
-// next row is under way while it works on this one, or two where rows are short (us with
-// 256 and 512: 32768x4096 bf16 153 and 157, fp32 284 and 303, 4096x16384 bf16 96 and 110;
-// 32768x1024 42 and 37, 32768x256 27 and 20, 8192x1280 fp32 32 and 28; with 1024 more but
-// for 32768x256, 22).
-inline uint32_t norm_grad_parts(uint32_t rows, uint32_t N) {
+// Workgroups that each keep the column sums of their share of the rows: two a CU, or
+// one, whose next row is under way while it works on this one, where a row of X and dY
+// takes 32 KB (pair_bytes: of a value of each) or more than 4096 values (us with 256
+// and 512: 32768x4096 bf16 153 to 170 and 156, fp32 285 and 304, 4096x16384 bf16 96 and 110,
+// 8192x5120 48 and 54; 32768x1024 42 and 37, 32768x256 27 and 20, 8192x1280 fp32 32
+// and 28; with 1024 more but for 32768x256, 22).
+inline uint32_t norm_grad_parts(uint32_t rows, uint32_t N, uint32_t pair_bytes) {
   if (N > kNormLong) return rows < 64u ? rows : 64u;
   const uint32_t once = norm_grad_rows_at_once(N), groups = (rows + once - 1) / once;
-  const uint32_t most = N <= 2048u ? 512u : 256u;
+  const uint32_t most = N <= 4096u && N * pair_bytes < 32768u ? 512u : 256u;
   return groups < most ? groups : most;
 }
 

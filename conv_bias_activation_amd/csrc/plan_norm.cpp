@@ -50,7 +50,8 @@ int plan_layer_norm(const void* X, const void* gamma, const void* beta, const vo
 
 size_t layer_norm_grad_workspace(int64_t rows, int64_t N) {
   if (rows <= 0 || N <= 0 || rows >= kMaxBytes || N >= kMaxBytes) return 0;
-  return (size_t)norm_grad_parts((uint32_t)rows, (uint32_t)N) * 2u * (size_t)N * 4u;
+  // (16-bit types have the most parts)
+  return (size_t)norm_grad_parts((uint32_t)rows, (uint32_t)N, 4u) * 2u * (size_t)N * 4u;
 }
 
 int plan_layer_norm_grad(const void* dY, const void* X, const void* gamma, const void* mean, const void* rstd,
