@@ -23,41 +23,34 @@ __device__ __forceinline__ float exp_neg(float x) {
 // dy GELU'(z) = dy (Phi(z) + z phi(z)).  For x = |z|, GELU'(-x) = phi(x) (M(x) - x)
 // and GELU'(x) = 1 - GELU'(-x), M the ratio of the normal distribution's tail to
 // its density, as t Q(t), t = 1 / (1 + a x) (fit_mills.py): one exponential for both
-// terms, and nothing cancels but at the slope's root.  fp32 tensors take x^2 in two
-// parts, so that the exponent's rounding does not show.  Below 2^-126 the result is formed
-// at 2^64 times its size, so that it rounds once (see exp2_f32).
+// terms, and nothing cancels but at the slope's root.  Q is the same for every type:
+// the bias's sums are fp32 whatever the type of dZ, and a degree that is enough for 16-bit dZ
+// (6: 4e-6 of M, 62 times 2^-24) leaves its error in them.  fp32 tensors take x^2 in two
+// parts, so that the exponent's rounding does not show; a 16-bit z has an exact x^2,
+// and what the exponent's own rounding leaves, 0.61 x^2 2^-24 of phi, is largest beside S
+// where phi counts for nothing in a sum (8192x16384 bf16 171 to 176 us with those four steps,
+// 162 to 164 without).  Below 2^-126 the result is formed at 2^64 times its size, so that
+// it rounds once (see exp2_f32).
 template <int DT>
 __device__ __forceinline__ float gelu_grad(float dy, float z) {
 #pragma clang fp contract(off)
-  constexpr bool F32 = DT == DT_F32;
   float x = __builtin_fabsf(z);
   x = x > 60.0f ? 60.0f : x;                           // (phi is zero from 15 on; infinity times it is not)
-  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(x, F32 ? 0.32f : 0.28f, 1.0f));
-  float q;
-  if constexpr (F32) {
-    q = -5.283590034e-02f;
-    q = __builtin_fmaf(q, t, 2.391539961e-01f);
-    q = __builtin_fmaf(q, t, -3.677475452e-01f);
-    q = __builtin_fmaf(q, t, 1.637595743e-01f);
-    q = __builtin_fmaf(q, t, -2.350982092e-02f);
-    q = __builtin_fmaf(q, t, 1.470248997e-01f);
-    q = __builtin_fmaf(q, t, 2.201547027e-01f);
-    q = __builtin_fmaf(q, t, 2.873156667e-01f);
-    q = __builtin_fmaf(q, t, 3.199985325e-01f);
-    q = __builtin_fmaf(q, t, 3.199999928e-01f);
-  } else {
-    q = -1.259118766e-01f;
-    q = __builtin_fmaf(q, t, 2.643102407e-01f);
-    q = __builtin_fmaf(q, t, 6.253626943e-02f);
-    q = __builtin_fmaf(q, t, 2.367679179e-01f);
-    q = __builtin_fmaf(q, t, 2.555146217e-01f);
-    q = __builtin_fmaf(q, t, 2.800923288e-01f);
-    q = __builtin_fmaf(q, t, 2.800000310e-01f);
-  }
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(x, 0.32f, 1.0f));
+  float q = -5.283590034e-02f;
+  q = __builtin_fmaf(q, t, 2.391539961e-01f);
+  q = __builtin_fmaf(q, t, -3.677475452e-01f);
+  q = __builtin_fmaf(q, t, 1.637595743e-01f);
+  q = __builtin_fmaf(q, t, -2.350982092e-02f);
+  q = __builtin_fmaf(q, t, 1.470248997e-01f);
+  q = __builtin_fmaf(q, t, 2.201547027e-01f);
+  q = __builtin_fmaf(q, t, 2.873156667e-01f);
+  q = __builtin_fmaf(q, t, 3.199985325e-01f);
+  q = __builtin_fmaf(q, t, 3.199999928e-01f);
   const float xx = x * x, e = xx * -0.721347511f;      // log2 e / 2 = 0.721347511 + 9.6298e-9
   const bool tiny = e < -126.0f;
   float r = __builtin_amdgcn_exp2f(tiny ? e + 64.0f : e);
-  if constexpr (F32) {
+  if constexpr (DT == DT_F32) {
     const float lo = __builtin_fmaf(x, x, -xx);
     const float c = __builtin_fmaf(lo, -0.721347511f, __builtin_fmaf(xx, -9.6298e-9f, __builtin_fmaf(xx, -0.721347511f, -e)));
     r = __builtin_fmaf(r, c * 0.693147181f, r);
@@ -91,7 +84,7 @@ __device__ __forceinline__ float act_grad(float dy, float z, float alpha) {
 // A lane holds eight columns, 2^lane_bits lanes share a row, and a workgroup
 // takes 256 >> lane_bits rows at once, walking down its share of them.  Bound by
 // memory: dY and Z are read once, dZ written once.  bf16, us with the sums' join, beside
-// a large copy's time for as many bytes (4.92 TB/s): 8192x16384 GELU 156 (164), 32768x4096
+// a large copy's time for as many bytes (4.92 TB/s): 8192x16384 GELU 162 (164), 32768x4096
 // LeakyReLU 151 (164), 1021x1003 tanh fp32 7.7, two launches.
 template <int DT>
 __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs a) {
