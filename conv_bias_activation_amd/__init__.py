@@ -10,7 +10,7 @@ this package raises ImportError — there is no fallback path.
     conv2d_bias_act(x, w, bias, y, strides=(1, 1), pads=(0, 0, 0, 0), dilations=(1, 1), act="tanh")
     gemm_bias_act_2k(..., workspace=ws) / conv2d_bias_act_2k(..., workspace=ws)
     mxfp4_quantize(X, codes, scales); gemm_mxfp4_bias_act(A, a_scales, B, b_scales, bias, C, act="gelu")
-    fp8_quantize(X, codes, scales); gemm_fp8_bias_act(A, a_scales, B, b_scales, bias, C, act="gelu", Z=Z)
+    fp8_quantize(X, codes, scales); gemm_fp8_bias_act(A, a_scales, B, b_scales, bias, C, act="gelu", Z=Z[, f32_sums=True])
     bias_act_grad(dY, Z, dZ, dbias, act="gelu", workspace=ws)
     layer_norm(X, gamma, beta, Y, mean, rstd); layer_norm_grad(dY, X, gamma, mean, rstd, dX, dgamma, dbeta, workspace=ws)
 """

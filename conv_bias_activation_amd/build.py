@@ -37,7 +37,8 @@ HIP_SOURCES = ["api.hip", "act_cast.hip", "dispatch.hip"] + [
     f"gemm_i8_{to}.hip" for to in ("f32", "f16", "bf16", "i32")] + [
     "mx_quant.hip"] + [f"gemm_mx_{ta}.hip" for ta in ("mxfp4", "f16", "bf16")] + [
     "api_f8.hip", "f8_quant.hip", "api_norm.hip", "act_grad.hip"] + [
-    f"{op}_{t}.hip" for op in ("gemm_f8", "layer_norm") for t in _TYPES]
+    f"{op}_{t}.hip" for op in ("gemm_f8", "layer_norm") for t in _TYPES] + [
+    f"gemm_f8_wide_{t}.hip" for t in ("f16", "bf16")]
 CPP_SOURCES = ["plan.cpp", "plan_mx.cpp", "plan_f8.cpp", "plan_norm.cpp"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-I", INCLUDE, "-I", CSRC, "-Wall",

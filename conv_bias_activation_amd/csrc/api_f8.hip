@@ -64,8 +64,8 @@ int gemm_impl(const void* A, const void* As, int a_block_rows, const void* B, co
   a.tiles_m = a.tiles_n = 0;       // set with the tile
   switch (p.dto) {
     case DT_F32: launch_gemm_f8_f32(a, s); break;
-    case DT_F16: launch_gemm_f8_f16(a, s); break;
-    default: launch_gemm_f8_bf16(a, s); break;
+    case DT_F16: p.wide ? launch_gemm_f8_wide_f16(a, s) : launch_gemm_f8_f16(a, s); break;
+    default: p.wide ? launch_gemm_f8_wide_bf16(a, s) : launch_gemm_f8_bf16(a, s); break;
   }
   return launch_status();
 }

@@ -15,7 +15,8 @@
 // Bound by the latency of loads and by reading B (8x4096x4096 bf16 4.2 us, of which a
 // launch 1.6 and B's 16.8 MB at 4.9 TB/s 3.4; 16x4096x16384 12.7; 8x16384x4096 12.4).  With 3
 // or 4 blocks under way the LDS holds one workgroup a CU: 8x4096x4096 4.3, 32x4096x4096 7.7
-// instead of 6.6; blocks dealt to the waves in turn made no difference.
+// instead of 6.6; blocks dealt to the waves in turn made no difference.  With fp32 sums
+// 8x4096x4096 4.3, 32x4096x4096 5.6 (5.3).
 #pragma once
 
 #include "gemm_f8_tile.hpp"
@@ -23,8 +24,8 @@
 namespace biasact {
 
 // NB, MB: blocks of 16 rows of B and A per wave; NW: waves along k; UN: blocks of
-// k that a wave has under way.
-template <int FA, int FB, int DTO, int NB, int MB, int NW, int UN>
+// k that a wave has under way.  WIDE: sums in fp32 throughout (gemm_f8_tile.hpp).
+template <int FA, int FB, int DTO, bool WIDE, int NB, int MB, int NW, int UN>
 __global__ __launch_bounds__(64 * NW) void f8_stream_kernel(F8GemmArgs a) {
   constexpr int TN = 16 * NB, TM = 16 * MB;
   // the waves' sums, [m][n] with n contiguous and 4 floats of padding a row,
@@ -105,7 +106,7 @@ __global__ __launch_bounds__(64 * NW) void f8_stream_kernel(F8GemmArgs a) {
           const f8::Frag bf = frag(i);
 #pragma unroll
           for (int j = 0; j < MB; ++j)
-            if constexpr (DTO == DT_F32) {
+            if constexpr (WIDE) {
 #pragma unroll
               for (int q = 0; q < 4; ++q)
                 acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f8::widen_part<FB>(bf, q, f8::scale_field(bs[u][i], 0)),
@@ -132,14 +133,14 @@ __global__ __launch_bounds__(64 * NW) void f8_stream_kernel(F8GemmArgs a) {
   out.store(a, smem, n0);
 }
 
-template <int DTO, int NB, int MB, int UN>
+template <int DTO, bool WIDE, int NB, int MB, int UN>
 inline void launch_f8_stream(F8GemmArgs a, hipStream_t s) {
   constexpr int NW = 8;
   a.tiles_n = (a.N + 16 * NB - 1) / (16 * NB);
   a.tiles_m = (a.M + 16 * MB - 1) / (16 * MB);
-  note_launch("gemm fp8 stream, %d n x %d m, k over %d waves", 16 * NB, 16 * MB, NW);
+  note_launch("gemm fp8 stream, %d n x %d m, k over %d waves%s", 16 * NB, 16 * MB, NW, WIDE ? ", fp32 sums" : "");
   f8::with_formats(a.fa, a.fb, [&](auto fa_c, auto fb_c) {
-    launch_kernel(f8_stream_kernel<decltype(fa_c)::value, decltype(fb_c)::value, DTO, NB, MB, NW, UN>,
+    launch_kernel(f8_stream_kernel<decltype(fa_c)::value, decltype(fb_c)::value, DTO, WIDE, NB, MB, NW, UN>,
                   dim3(a.tiles_m * a.tiles_n), dim3(64 * NW), s, a);
   });
 }
@@ -188,24 +189,24 @@ inline int f8_choice(const F8GemmArgs& a, bool large) {
   return best;
 }
 
-// (An fp32 output's widened operands leave no registers for the largest tile.)
-template <int DTO>
+// (Widened operands leave no registers for the largest tile.)
+template <int DTO, bool WIDE>
 inline void launch_gemm_f8(const F8GemmArgs& a, hipStream_t s) {
-  switch (f8_choice(a, DTO != DT_F32)) {
-    case kF8Stream16: return launch_f8_stream<DTO, 1, 1, 2>(a, s);
-    case kF8Stream32: return launch_f8_stream<DTO, 2, 1, 2>(a, s);
-    case kF8Wave32: return launch_f8_tile<DTO, 1, 1, 2, 1, 4, 2>(a, s);
-    case kF8Wave64: return launch_f8_tile<DTO, 1, 1, 2, 2, 4, 2>(a, s);
-    case kF8Tile64: return launch_f8_tile<DTO, 1, 2, 2, 1, 1, 4>(a, s);
+  switch (f8_choice(a, !WIDE)) {
+    case kF8Stream16: return launch_f8_stream<DTO, WIDE, 1, 1, 2>(a, s);
+    case kF8Stream32: return launch_f8_stream<DTO, WIDE, 2, 1, 2>(a, s);
+    case kF8Wave32: return launch_f8_tile<DTO, WIDE, 1, 1, 2, 1, 4, 2>(a, s);
+    case kF8Wave64: return launch_f8_tile<DTO, WIDE, 1, 1, 2, 2, 4, 2>(a, s);
+    case kF8Tile64: return launch_f8_tile<DTO, WIDE, 1, 2, 2, 1, 1, 4>(a, s);
     case kF8TileDeep:
       // Operands of 64 MB and more are seldom in the last-level cache (us, bf16, out of
       // it and in it: 1024x4096x16384, 84 MB, 90 and 63, with the wave ahead 70 and 68;
       // 1024x4096x4096, 21 MB, 26 and 19, 23 and 21).
-      if ((uint64_t)a.a_bytes + a.b_bytes >= 1u << 26) return launch_f8_tile<DTO, 2, 2, 2, 2, 1, 4, true>(a, s);
-      return launch_f8_tile<DTO, 2, 2, 2, 2, 1, 4>(a, s);
-    case kF8TileTwice: return launch_f8_tile<DTO, 2, 2, 2, 2, 1, 2>(a, s);
+      if ((uint64_t)a.a_bytes + a.b_bytes >= 1u << 26) return launch_f8_tile<DTO, WIDE, 2, 2, 2, 2, 1, 4, true>(a, s);
+      return launch_f8_tile<DTO, WIDE, 2, 2, 2, 2, 1, 4>(a, s);
+    case kF8TileTwice: return launch_f8_tile<DTO, WIDE, 2, 2, 2, 2, 1, 2>(a, s);
     default:
-      if constexpr (DTO != DT_F32) launch_f8_tile<DTO, 2, 4, 4, 2, 1, 2>(a, s);
+      if constexpr (!WIDE) launch_f8_tile<DTO, WIDE, 2, 4, 4, 2, 1, 2>(a, s);
   }
 }
 

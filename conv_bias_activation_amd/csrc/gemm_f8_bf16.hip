@@ -2,5 +2,5 @@
 #include "gemm_f8.hpp"
 
 namespace biasact {
-void launch_gemm_f8_bf16(const F8GemmArgs& a, hipStream_t s) { launch_gemm_f8<DT_BF16>(a, s); }
+void launch_gemm_f8_bf16(const F8GemmArgs& a, hipStream_t s) { launch_gemm_f8<DT_BF16, false>(a, s); }
 }  // namespace biasact

@@ -2,5 +2,5 @@
 #include "gemm_f8.hpp"
 
 namespace biasact {
-void launch_gemm_f8_f32(const F8GemmArgs& a, hipStream_t s) { launch_gemm_f8<DT_F32>(a, s); }
+void launch_gemm_f8_f32(const F8GemmArgs& a, hipStream_t s) { launch_gemm_f8<DT_F32, true>(a, s); }
 }  // namespace biasact

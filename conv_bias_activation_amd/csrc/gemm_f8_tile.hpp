@@ -20,7 +20,8 @@
 // cycles are LDS reads of operands, without conflicts that matter, a quarter direct loads.
 // Round it lie 10 us of first loads, epilogue and stores.  bf16 outputs: 4096^3 55 us (2490
 // TFLOP/s), with GELU 62, 4096x4096x16384 188 (2920), 8192^3 377 to 386 (2850 to 2920), 32768x1024x4096
-// 105 (2630); fp32 outputs 4096^3 108 to 114.  Four waves of 128x128 63 (one wave a
+// 105 (2630).  With fp32 sums (WIDE): 4096^3 108 to 114, 32768x1024x4096 213, 4096x1024x32768
+// 228, 1024x4096x4096 34 (20), 256x4096x4096 18 (10), 64x4096x4096 7.7 (7.0).  Four waves of 128x128 63 (one wave a
 // SIMD hides nothing), all loads of a step at once 57, other priorities the same.
 //
 // Registers: 128 sums a lane at 4 x 2 blocks, and the operands of two quarters of
@@ -67,11 +68,15 @@ __device__ __forceinline__ f32x4 mfma16(const Frag& b, const Frag& a, f32x4 acc,
 // ---- products whose sums are to be fp32 throughout -----------------------------------
 // The 8-bit instructions above add eight neighbouring products in fixed point: each is
 // cut off below 2^(e - 13), e the largest sum of two exponents among the eight
-// (measured on single products: 2^2 beside 2^16 vanishes, 2^3 stays), which
-// leaves a result of many terms 5e-5 off (2-norm) without a bias.  A 16-bit output rounds
-// by 2e-4 or more; an fp32 output would show it, so there the codes are widened
-// to bf16 with their scale, which is exact within bf16's range, and bf16
-// instructions form the sums, at half the rate.
+// (measured on single products: 2^2 beside 2^16 vanishes, 2^3 stays), towards zero.  A
+// result is off by less than 7 * 2^-13 times the sum of the eights' largest powers, whatever
+// its own size, and terms of one sign are off in one direction.  Normal values lose 1.5e-5 of the
+// result (2-norm), channels of unlike size 5e-5, where a 16-bit output rounds by 2e-4 or more;
+// sums of one sign with an eighth of the channels 400 times the others come out 1.5e-4
+// low, and where those channels cancel, 1.6e-2.  An fp32 output would show the
+// first already, and a caller may want a 16-bit one without the last: for both (WIDE)
+// the codes are widened to bf16 with their scale, which is exact within bf16's range,
+// and bf16 instructions form the sums, at half the rate.
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
@@ -153,7 +158,7 @@ constexpr int wait_vm(int n) { return 0x0F70 | (n & 0xF) | ((n >> 4) << 14); }
 // 4096x1024x32768 with the operands out of the last-level cache 195 -> 152 us, from
 // it 129 -> 141.  (The others' own loads, three steps ahead, would have to be waited for
 // in order; this wave waits for none.)
-template <int FA, int FB, int DTO, int WM, int WN, int SJ, int SI, int KG, int ST, bool AHEAD>
+template <int FA, int FB, int DTO, bool WIDE, int WM, int WN, int SJ, int SI, int KG, int ST, bool AHEAD>
 __global__ __launch_bounds__(64 * (WM * WN * KG + AHEAD), (AHEAD ? 1 : f8::Tile<WM, WN, SJ, SI, KG, ST>::WAVES)) void f8_tile_kernel(F8GemmArgs a) {
   using T = f8::Tile<WM, WN, SJ, SI, KG, ST>;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[T::LDS_BYTES + (AHEAD ? 256 : 0)];
@@ -281,7 +286,6 @@ __global__ __launch_bounds__(64 * (WM * WN * KG + AHEAD), (AHEAD ? 1 : f8::Tile<
     *reinterpret_cast<float*>(smem + T::BIAS_OFF + threadIdx.x * 4) =
         a.bias_dt == DT_F16 ? widen<DT_F16>(bias) : a.bias_dt == DT_BF16 ? widen<DT_BF16>(bias) : widen<DT_F32>(bias);
   const uint32_t sc_rd = T::S_OFF + lrow * 4;
-  constexpr bool WIDE = DTO == DT_F32;
   constexpr int HJ = SJ / 2;                           // blocks of A's rows a quarter
   f8::Frag fa[2][HJ], fb[2][SI];                       // by half of A's rows; by k-half
   uint32_t wa[2][SJ], wb[2][SI];                       // scale words, by parity of the word
@@ -401,14 +405,15 @@ __global__ __launch_bounds__(64 * (WM * WN * KG + AHEAD), (AHEAD ? 1 : f8::Tile<
   }
 }
 
-template <int DTO, int WM, int WN, int SJ, int SI, int KG, int ST, bool AHEAD = false>
+template <int DTO, bool WIDE, int WM, int WN, int SJ, int SI, int KG, int ST, bool AHEAD = false>
 inline void launch_f8_tile(F8GemmArgs a, hipStream_t s) {
   using T = f8::Tile<WM, WN, SJ, SI, KG, ST>;
   a.tiles_n = (a.N + T::BN - 1) / T::BN;
   a.tiles_m = (a.M + T::BM - 1) / T::BM;
-  note_launch("gemm fp8 tile, %d m x %d n, k over %d groups of waves, %d stages%s", T::BM, T::BN, KG, ST, AHEAD ? ", a wave ahead" : "");
+  note_launch("gemm fp8 tile, %d m x %d n, k over %d groups of waves, %d stages%s%s", T::BM, T::BN, KG, ST, AHEAD ? ", a wave ahead" : "",
+              WIDE ? ", fp32 sums" : "");
   f8::with_formats(a.fa, a.fb, [&](auto fa_c, auto fb_c) {
-    launch_kernel(f8_tile_kernel<decltype(fa_c)::value, decltype(fb_c)::value, DTO, WM, WN, SJ, SI, KG, ST, AHEAD>,
+    launch_kernel(f8_tile_kernel<decltype(fa_c)::value, decltype(fb_c)::value, DTO, WIDE, WM, WN, SJ, SI, KG, ST, AHEAD>,
                   dim3(a.tiles_m * a.tiles_n), dim3(T::THREADS + (AHEAD ? 64 : 0)), s, a);
   });
 }

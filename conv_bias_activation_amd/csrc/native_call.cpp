@@ -185,6 +185,7 @@ int f8_quantize(PyObject* const* a) {
 }
 
 // (A, a_scales, B, b_scales, bias or None, R or None, Z or None, C, act, alpha)
+template <uint32_t SUMS>
 int f8_gemm(PyObject* const* a) {
   const at::Tensor *A = tensor(a[0]), *B = tensor(a[2]), *C = tensor(a[7]);
   int64_t M, N, ka, kb;
@@ -201,7 +202,7 @@ int f8_gemm(PyObject* const* a) {
   const int act = act_code(a[8]);
   if (act < 0 || !PyFloat_CheckExact(a[9])) return kNotTaken;
   const float alpha = (float)PyFloat_AS_DOUBLE(a[9]);
-  const uint32_t dt = BA_DTYPES(f8_code(*A), f8_code(*B), tb < 0 ? BA_F32 : tb, tc);
+  const uint32_t dt = BA_DTYPES(f8_code(*A), f8_code(*B), tb < 0 ? BA_F32 : tb, (uint32_t)tc | SUMS);
   return a[5] != Py_None
              ? p_f8_gemm_add(A->data_ptr(), As->data_ptr(), block_a, B->data_ptr(), Bs->data_ptr(), block_b, bias, rp, zp,
                              C->data_ptr(), M, N, 128 * ka, dt, act, alpha, current_stream())
@@ -343,7 +344,8 @@ PyMethodDef methods[] = {
     {"bind_layer", as_method(&bind_layer), METH_FASTCALL, nullptr},
     {"f8_quantize", as_method(&call<f8_quantize<false>, 4>), METH_FASTCALL, nullptr},
     {"f8_dequantize", as_method(&call<f8_quantize<true>, 4>), METH_FASTCALL, nullptr},
-    {"f8_gemm", as_method(&call<f8_gemm, 10>), METH_FASTCALL, nullptr},
+    {"f8_gemm", as_method(&call<f8_gemm<0u>, 10>), METH_FASTCALL, nullptr},
+    {"f8_gemm_f32_sums", as_method(&call<f8_gemm<BA_SUMS_F32>, 10>), METH_FASTCALL, nullptr},
     {"act_grad", as_method(&call<act_grad, 7>), METH_FASTCALL, nullptr},
     {"norm", as_method(&call<norm, 7>), METH_FASTCALL, nullptr},
     {"norm_grad", as_method(&call<norm_grad, 9>), METH_FASTCALL, nullptr},

@@ -90,6 +90,7 @@ struct F8GemmPlan {
   int fa, fb, dto, bias_dt;        // bias_dt = -1 without bias
   uint32_t M, N, KB, KW, ash, bsh;
   uint32_t a_bytes, as_bytes, b_bytes, bs_bytes, bias_bytes, c_bytes;
+  bool wide;                       // sums in fp32 for a 16-bit output too
   bool empty;                      // M == 0 or N == 0: nothing to launch
 };
 

@@ -8,6 +8,7 @@ namespace biasact {
 namespace {
 
 constexpr int kF32 = 0, kF16 = 1, kBF16 = 2, kE4m3 = 6, kE5m2 = 7;
+constexpr int kSumsF32 = 0x40;                    // BA_SUMS_F32, beside the output's code
 constexpr int64_t kMaxBytes = (int64_t)1 << 31;   // every tensor < 2 GiB (32-bit buffer offsets)
 
 int elem_bytes(int dt) { return dt == kF32 ? 4 : 2; }
@@ -72,7 +73,8 @@ int plan_f8_gemm(const void* A, const void* As, int a_block_rows, const void* B,
   if (act < 0 || act > 5) return kErrInvalid;
   if ((a_block_rows != 1 && a_block_rows != 128) || (b_block_rows != 1 && b_block_rows != 128)) return kErrInvalid;
   const int a = (int)(dtypes & 0xffu), b = (int)((dtypes >> 8) & 0xffu);
-  const int dtb = (int)((dtypes >> 16) & 0xffu), out = (int)((dtypes >> 24) & 0xffu);
+  const int dtb = (int)((dtypes >> 16) & 0xffu), out = (int)((dtypes >> 24) & 0xffu & ~(uint32_t)kSumsF32);
+  p->wide = ((dtypes >> 24) & (uint32_t)kSumsF32) != 0;
   if (!valid_f8(a) || !valid_f8(b) || !valid_float_dt(out) || (bias && !valid_float_dt(dtb))) return kErrUnsupported;
   if (M >= kMaxBytes || N >= kMaxBytes || K >= kMaxBytes) return kErrUnsupported;
   const int64_t so = elem_bytes(out);

@@ -63,6 +63,7 @@ extern "C" {
 #define BA_MXFP4 5u         /* 4-bit floating point in scaled blocks (below): gemm_mxfp4_* operands only */
 #define BA_F8E4M3 6u        /* 8-bit floating point in scaled blocks (below): fp8_* and gemm_fp8_* operands only, */
 #define BA_F8E5M2 7u        /* 4 exponent and 3 mantissa bits (OCP e4m3), or 5 and 2 */
+#define BA_SUMS_F32 0x40u   /* or-ed to gemm_fp8_*'s code of C: sums in fp32 for a 16-bit C too (below) */
 
 /* dtypes argument: one 8-bit code per operand.
  *   a   : A (GEMM) or x (conv)
@@ -291,17 +292,27 @@ int fp8_dequantize(const void* codes, const void* scales, void* Y, int64_t rows,
 /* C[M,N] = act(A[M,K] . B[N,K]^T + bias[N])  and  act(A . B^T + bias + R), both
  * operands in 8 bits as above (dtypes' a and b: BA_F8E4M3 or BA_F8E5M2, in any
  * combination), each with its own block_rows.  bias and out: fp32, fp16 or bf16
- * each; R has C's type and shape and may be C itself.  Z, where it is not NULL,
- * takes A . B^T + bias (+ R) in C's type and shape, which a backward pass needs
- * (bias_act_grad); it must not overlap C or R (BA_ERR_INVALID where it is one of
- * them).  Bias, residual and activation run in fp32 with one rounding each to C and to Z.
- * With an fp32 C the products are exact and their sum is fp32, over the operands' values
- * as bf16 holds them (exactly, where they lie below 2^128 and are no multiples of less than 2^-133).
- * With a 16-bit C the 8-bit matrix instructions form the sum, twice as fast: they
- * add the products of eight neighbouring k in fixed point, each cut off at 2^-13 of the
- * power of two that the largest product's exponents give, and the rest in fp32; on a sum of
- * many terms that is some 5e-5 of its size (2-norm), below half a step of the output.
- * The order of a sum depends on the sizes and types alone, so equal calls give equal bits.  A value that is not finite affects its row (of
+ * each (out may have BA_SUMS_F32 beside it); R has C's type and shape and may be C
+ * itself.  Z, where it is not NULL, takes A . B^T + bias (+ R) in C's type and shape,
+ * which a backward pass needs (bias_act_grad); it must not overlap C or R
+ * (BA_ERR_INVALID where it is one of them).  Bias, residual and activation run in
+ * fp32 with one rounding each to C and to Z.
+ * With an fp32 C, or with BA_SUMS_F32, the products are exact and their sum is fp32,
+ * over the operands' values as bf16 holds them (exactly, where they lie below 2^128
+ * and are no multiples of less than 2^-133).
+ * With a 16-bit C and without BA_SUMS_F32 the 8-bit matrix instructions form the sum,
+ * up to twice as fast: they add the products of eight neighbouring k (8 j .. 8 j + 7)
+ * in fixed point, each cut off, towards zero, at 2^-13 of p_j, and the rest in fp32.
+ * p_j is the largest of the eight products of the operands' powers of two (2^e for a
+ * value of 1.f 2^e, the smallest normal one for a subnormal code).  The sum is off by less than 7 * 2^-13 * sum over j of p_j for that,
+ * whatever its own size, and terms of one sign are all off in one direction.
+ * Normal values of like size lose 1.5e-5 of the result (2-norm), channels of unlike
+ * size 5e-5, less than half a step of C.  But with an eighth of the channels 400 times
+ * the others, sums of one sign come out 1.5e-4 low, and where those channels cancel
+ * and the others are the result, 1.6e-2 (2.4e-3 with channels of 100 times), several
+ * steps of C: such sums want BA_SUMS_F32.
+ * The order of a sum depends on the sizes and types alone, so equal calls give equal
+ * bits.  A value that is not finite affects its row (of
  * A) or column (of B) only.  M, N, K >= 0 (M or N == 0: nothing to do; K == 0:
  * C = act(bias (+ R))).  The gradients of act(X W^T + bias) are two more such
  * products: dX = dZ . W, over operands dZ [M,N] and W^T [K,N], and dW = dZ^T . X,
