@@ -199,10 +199,17 @@ inline void launch_gemm_f8(const F8GemmArgs& a, hipStream_t s) {
     case kF8Wave64: return launch_f8_tile<DTO, WIDE, 1, 1, 2, 2, 4, 2>(a, s);
     case kF8Tile64: return launch_f8_tile<DTO, WIDE, 1, 2, 2, 1, 1, 4>(a, s);
     case kF8TileDeep:
-      // Operands of 64 MB and more are seldom in the last-level cache (us, bf16, out of
-      // it and in it: 1024x4096x16384, 84 MB, 90 and 63, with the wave ahead 70 and 68;
-      // 1024x4096x4096, 21 MB, 26 and 19, 23 and 21).
-      if ((uint64_t)a.a_bytes + a.b_bytes >= 1u << 26) return launch_f8_tile<DTO, WIDE, 2, 2, 2, 2, 1, 4, true>(a, s);
+      // A wave ahead for operands of 64 MB and more, of which a part at least has left the
+      // last-level cache by the time they are used, and three columns of tiles or more
+      // (with fewer, its shares leave out most of A's rows).  us, bf16, with operands that take turns
+      // out of that cache, without and with it, and then the same in the cache:
+      //   4096x1024x32768 157 and 147, 125 and 136; 1024x4096x16384 78 and 75, 66 and 71;
+      //   2048x2048x16384 75 and 73, 65 and 69; 8192x512x16384 83 and 79, 66 and 71
+      //   4 rows of tiles: 512x8192x16384 82 and 85, 67 and 72; 2: 256x16384x8192 52 and 53, 37 and 39
+      //   2 columns: 16384x256x8192 53 and 53, 38 and 41; 1: 32768x128x8192 74 and 71, 50 and 60
+      // In a backward pass, whose operands were just quantised, it gives 20 us (32768x4096x1024
+      // with dW of 4096x1024x32768: 593 and 573).
+      if (a.N > 256 && (uint64_t)a.a_bytes + a.b_bytes >= 1u << 26) return launch_f8_tile<DTO, WIDE, 2, 2, 2, 2, 1, 4, true>(a, s);
       return launch_f8_tile<DTO, WIDE, 2, 2, 2, 2, 1, 4>(a, s);
     case kF8TileTwice: return launch_f8_tile<DTO, WIDE, 2, 2, 2, 2, 1, 2>(a, s);
     default:

@@ -155,8 +155,9 @@ constexpr int wait_vm(int n) { return 0x0F70 | (n & 0xF) | ((n >> 4) << 14); }
 // at once, which HBM gives faster than one every step, and only the workgroup's share
 // of them, since an XCD that works on 8 x 4 tiles wants each line of A four times and
 // each of B eight times.  (Where it works on others, some lines come late, as without.)
-// 4096x1024x32768 with the operands out of the last-level cache 195 -> 152 us, from
-// it 129 -> 141.  (The others' own loads, three steps ahead, would have to be waited for
+// 4096x1024x32768 with operands that take turns out of the last-level cache 157 -> 147 us,
+// behind a fill of 512 MB that is still being written back 195 -> 152, from the cache
+// 125 -> 136; launch_gemm_f8 says when.  (The others' own loads, three steps ahead, would have to be waited for
 // in order; this wave waits for none.)
 template <int FA, int FB, int DTO, bool WIDE, int WM, int WN, int SJ, int SI, int KG, int ST, bool AHEAD>
 __global__ __launch_bounds__(64 * (WM * WN * KG + AHEAD), (AHEAD ? 1 : f8::Tile<WM, WN, SJ, SI, KG, ST>::WAVES)) void f8_tile_kernel(F8GemmArgs a) {

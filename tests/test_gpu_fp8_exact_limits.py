@@ -68,3 +68,17 @@ def test_operand_of_two_gib(ba, rows, K, other, fmt, block_rows, every, left, ou
         part = slice(i, min(i + step, rows))
         ref = torch.matmul(values(*big, part, block_rows), w.t().contiguous())
         assert torch.equal(got[part], ref.to(out)), (i, ba.last_tile_config())
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,N,K,ahead", [(17000, 128, 4096, False), (20000, 100, 4000, False), (16300, 200, 4500, False), (10000, 300, 6800, True)])
+def test_products_of_one_round_and_few_columns(ba, M, N, K, ahead, out):
+    # operands of 64 MB and more; one or two columns of tiles have no wave ahead
+    a, b = operand(M, K, "f8e4m3", 1, 4, 0), operand(N, K, "f8e5m2", 128, 4, 1)
+    C = torch.full((M, N), 7.0, dtype=out, device="cuda")
+    ba.gemm_fp8_bias_act(*a, *b, None, C)
+    assert "4 stages" in ba.last_tile_config() and ("a wave ahead" in ba.last_tile_config()) == ahead
+    one = torch.where(b[0].view(torch.uint8) == 0, 0.0, torch.where(b[0].view(torch.uint8) >= 128, -1.0, 1.0))
+    s = torch.exp2(b[1].float() - 127).round()[torch.arange(N, device="cuda") // 128][:, :one.shape[1] // 128]
+    w = (one.view(N, -1, 128) * s[:, :, None]).view(N, -1)
+    assert torch.equal(C, torch.matmul(values(*a, slice(0, M), 1), w.t().contiguous()).to(out))
