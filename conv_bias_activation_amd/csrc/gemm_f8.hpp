@@ -12,11 +12,13 @@
 // r lies at slot c ^ (r / 2 % 8).  Lane (r, g) takes the chunks g and 4 + g of row r:
 // any assignment will do that is the same for both operands, since a block has one scale.
 //
-// Bound by the latency of loads and by reading B (8x4096x4096 bf16 4.2 us, of which a
-// launch 1.6 and B's 16.8 MB at 4.9 TB/s 3.4; 16x4096x16384 12.7; 8x16384x4096 12.4).  With 3
-// or 4 blocks under way the LDS holds one workgroup a CU: 8x4096x4096 4.3, 32x4096x4096 7.7
-// instead of 6.6; blocks dealt to the waves in turn made no difference.  With fp32 sums
-// 8x4096x4096 4.3, 32x4096x4096 5.6 (5.3).
+// Bound by the latency of loads and by reading B: 8x4096x4096 bf16 takes 4.2 us with B in the
+// last-level cache and 6.1 with B out of it, whose 16.8 MB are 3.4 us at a large copy's
+// 4.9 TB/s; 16x4096x4096 4.7 and 6.5; with Z, a residual and GELU 4.5 and 4.9.  (From
+// that cache: 16x4096x16384 12.7, 8x16384x4096 12.4.)  With 3 or 4 blocks under way the LDS
+// holds one workgroup a CU: 8x4096x4096 4.3, 32x4096x4096 7.7 instead of 6.6; blocks dealt
+// to the waves in turn made no difference.  With fp32 sums 8x4096x4096 4.3,
+// 32x4096x4096 5.6 (5.3).
 #pragma once
 
 #include "gemm_f8_tile.hpp"
@@ -147,7 +149,8 @@ inline void launch_f8_stream(F8GemmArgs a, hipStream_t s) {
 
 // Choice of the kernel: the least estimated time.  Each kernel's workgroups take
 // the 256 CUs in rounds, and a round takes a part of its own and one for each
-// block of k.  The estimates, in 10 ns, fit these measurements (us, bf16 outputs):
+// block of k.  The estimates, in 10 ns, fit these measurements (us, bf16 outputs,
+// operands from the last-level cache):
 //   stream 16x16          8x4096x4096 4.2, 16x4096x16384 12.7, 64x4096x4096 10.9, 256x4096x1024 15.9
 //   stream 32 n x 16 m    32x4096x4096 5.3, 64x4096x4096 9.0
 //   wave   64 m x 32 n    64x4096x4096 7.1, 256x4096x4096 13.6, 64x1024x16384 16.4

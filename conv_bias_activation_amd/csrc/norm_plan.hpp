@@ -36,7 +36,8 @@ inline uint32_t norm_grad_parts(uint32_t rows, uint32_t N, uint32_t pair_bytes) 
 
 // Lanes (as a power of two) that share a row of N values in bias_act_grad, eight
 // columns a lane, and the row splits for M rows: up to 1024 workgroups, four a CU (us,
-// bf16: 8192x16384 GELU 158, with 2048 171, 4096 166; 32768x4096 LeakyReLU 151, 165, 168).
+// bf16: 8192x16384 GELU 163, with 512 200, 2048 167, 4096 167; 32768x4096 LeakyReLU 151, with
+// 2048 165, 4096 168).
 inline uint32_t act_grad_lane_bits(uint32_t N) {
   uint32_t b = 0;
   while (b < 6u && (8u << b) < N) ++b;

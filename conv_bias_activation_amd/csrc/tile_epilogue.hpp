@@ -7,7 +7,9 @@
 // accesses over the banks), from where it stores pieces of whole cache lines, 16
 // bytes a lane.  A residual comes in the same way, its loads 32 rows ahead.  No barrier
 // holds up one wave's stores for another's arithmetic.  The sums before the
-// activation (Z) leave by a round of their own before C's.  With two barriers for every 32
+// activation (Z) leave by a round of their own before C's, which reads the residual
+// again.  4096^3 bf16, us in a trace: 57, with GELU and Z 67, with a residual 70, with
+// GELU, Z and a residual 94 (each of Z and R is 33.6 MB, 6.8 us at a large copy's rate).  With two barriers for every 32
 // rows instead, 4096^3 with GELU took 63.2 us (61.7) and 32768x4096x1024 158 (154).
 #pragma once
 
