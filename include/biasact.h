@@ -306,11 +306,12 @@ int fp8_dequantize(const void* codes, const void* scales, void* Y, int64_t rows,
  * p_j is the largest of the eight products of the operands' powers of two (2^e for a
  * value of 1.f 2^e, the smallest normal one for a subnormal code).  The sum is off by less than 7 * 2^-13 * sum over j of p_j for that,
  * whatever its own size, and terms of one sign are all off in one direction.
- * Normal values of like size lose 1.5e-5 of the result (2-norm), channels of unlike
- * size 5e-5, less than half a step of C.  But with an eighth of the channels 400 times
- * the others, sums of one sign come out 1.5e-4 low, and where those channels cancel
- * and the others are the result, 1.6e-2 (2.4e-3 with channels of 100 times), several
- * steps of C: such sums want BA_SUMS_F32.
+ * Normal values of like size are off by 1.5e-5 of the results' 2-norm, channels of
+ * unlike size (log-normal, one in a hundred 20 times larger) by 6e-5, less than half a
+ * step of most results (one near zero among them is off by as much as the others).
+ * But with an eighth of the channels 400 times the others, sums of one sign come out
+ * 1.5e-4 low, and where those channels cancel and the others are the result, 1.6e-2
+ * (2.4e-3 with channels of 100 times), several steps of C: such sums want BA_SUMS_F32.
  * The order of a sum depends on the sizes and types alone, so equal calls give equal
  * bits.  A value that is not finite affects its row (of
  * A) or column (of B) only.  M, N, K >= 0 (M or N == 0: nothing to do; K == 0:
