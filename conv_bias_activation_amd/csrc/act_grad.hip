@@ -27,8 +27,8 @@ __device__ __forceinline__ float exp_neg(float x) {
 // the bias's sums are fp32 whatever the type of dZ, and a degree that is enough for 16-bit dZ
 // (6: 4e-6 of M, 62 times 2^-24) leaves its error in them.  fp32 tensors take x^2 in two
 // parts, so that the exponent's rounding does not show; a 16-bit z has an exact x^2,
-// and what the exponent's own rounding leaves, 0.61 x^2 2^-24 of phi, is largest beside S
-// where phi counts for nothing in a sum (8192x16384 bf16 171 to 176 us with those four steps,
+// and what the exponent's own rounding leaves, 0.61 x^2 2^-24 of phi, is large only
+// where phi counts for nothing in a sum (8192x16384 bf16 171 to 176 us with those steps,
 // 162 to 164 without).  Below 2^-126 the result is formed at 2^64 times its size, so that
 // it rounds once (see exp2_f32).
 template <int DT>
